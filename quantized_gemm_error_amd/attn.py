@@ -1,0 +1,404 @@
+"""Binding of libspear's paged key-value cache and attention (include/spear_attn.h), same names
+as the C ABI.
+
+Argument marshalling and checks only, as in spear.py: every step runs in the library's HIP
+kernels, and there is no fallback.  The handles (SpearKVCache, SpearKVBatch, SpearKVPool) check
+their tensors once and keep the C structs; a program makes the cache's and the pool's once and the
+batch's once per step, for all layers.  They hold references to their tensors and read no values
+from them.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+
+from . import spear
+from .spear import SpearError, _check, _require, SPEAR_ERR_INVALID_ARGUMENT
+
+SPEAR_ATTN_MAX_SEQS = 4096
+SPEAR_KV_MAX_ENTRIES = 1024
+
+# Every function the header declares, for the export check.
+EXPORTED = (
+    "spear_attn_workspace_bytes", "spear_attn_decode", "spear_attn_prefill", "spear_kv_append",
+    "spear_kv_copy_pages", "spear_kv_scratch_words", "spear_kv_fork", "spear_kv_reserve",
+    "spear_kv_free", "spear_kv_compact",
+)
+
+_P, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+
+
+class SpearKVCacheC(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("dtype", _i32), ("n_layers", _i32), ("num_pages", _i32),
+                ("n_kv_heads", _i32), ("page_size", _i32), ("head_dim", _i32),
+                ("stride_layer", _i64), ("stride_page", _i64), ("stride_head", _i64),
+                ("stride_token", _i64)]
+
+
+class SpearKVBatchC(ctypes.Structure):
+    _fields_ = [("n_seqs", _i32), ("table_width", _i32), ("n_tokens", _i32),
+                ("block_table", _P), ("kv_lens", _P), ("q_starts", _P)]
+
+
+class SpearAttnArgsC(ctypes.Structure):
+    _fields_ = [("n_q_heads", _i32), ("window", _i32), ("sinks", _i32), ("scale", ctypes.c_float),
+                ("q", _P), ("q_stride_token", _i64), ("q_stride_head", _i64),
+                ("out", _P), ("out_stride_token", _i64), ("out_stride_head", _i64), ("lse", _P)]
+
+
+class SpearKVPoolC(ctypes.Structure):
+    _fields_ = [("num_pages", _i32), ("page_size", _i32), ("n_slots", _i32), ("table_width", _i32),
+                ("refs", _P), ("table", _P), ("lens", _P), ("scratch", _P)]
+
+
+_bound = None
+
+
+def load_library():
+    """libspear.so with this header's functions declared (raises if it has not been built)."""
+    global _bound
+    if _bound is not None:
+        return _bound
+    lib = spear.load_library()
+    C, B, A = (ctypes.POINTER(t) for t in (SpearKVCacheC, SpearKVBatchC, SpearAttnArgsC))
+    L = ctypes.POINTER(SpearKVPoolC)
+    lib.spear_attn_workspace_bytes.argtypes = [C, _i32, _i32, _i32]
+    lib.spear_attn_workspace_bytes.restype = _sz
+    lib.spear_attn_decode.argtypes = [C, B, A, _P, _sz, _P]
+    lib.spear_attn_prefill.argtypes = [C, B, A, _P, _sz, _P]
+    lib.spear_kv_append.argtypes = [C, B, _P, _P, _i64, _i64, _i64, _i64, _P]
+    lib.spear_kv_copy_pages.argtypes = [C, _P, _P, _i32, _P]
+    lib.spear_kv_scratch_words.argtypes = [_i32, _i32, _i32]
+    lib.spear_kv_scratch_words.restype = _sz
+    lib.spear_kv_fork.argtypes = [L, _P, _P, _i32, _P]
+    lib.spear_kv_reserve.argtypes = [L, C, _P, _P, _i32, _P, _P]
+    lib.spear_kv_free.argtypes = [L, _P, _i32, _P]
+    lib.spear_kv_compact.argtypes = [L, C, _P, _P]
+    for name in EXPORTED:
+        if name not in ("spear_attn_workspace_bytes", "spear_kv_scratch_words"):
+            getattr(lib, name).restype = _i32
+    _bound = lib
+    return lib
+
+
+def _int32(t, name: str, dim: int, device=None) -> None:
+    import torch
+    _require(t is not None, f"{name} is missing")
+    _require(t.dtype == torch.int32, f"{name} has dtype {t.dtype}, expected torch.int32", TypeError)
+    _require(t.dim() == dim and t.is_contiguous(), f"{name} must be a contiguous {dim}-D tensor")
+    if device is not None:
+        _require(t.device == device, f"{name} is on {t.device}, expected {device}")
+
+
+def _gpu(device) -> None:
+    _require(device.type == "cuda", f"tensors must be on a GPU, got {device}")
+
+
+class _On:
+    """The stream a call runs on; its device is made the current one for the call."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.given = stream is not None
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        self.stream = stream
+        self.ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        self.guard = None if torch.cuda.current_device() == device.index else \
+            torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def made(self, *tensors):
+        """Tensors allocated by the call (on the current stream) and written on a given one."""
+        if self.given:
+            import torch
+            st = self.stream
+            if not hasattr(st, "cuda_stream"):
+                st = torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()
+            here = torch.cuda.current_stream(tensors[0].device)
+            if st.cuda_stream != here.cuda_stream:
+                st.wait_stream(here)  # what the memory served before ends first
+                for t in tensors:
+                    t.record_stream(st)
+
+
+class SpearKVCache:
+    """The pages of one layer ([pages][kv heads][page][dim]) or of all layers (a leading layer
+    dimension): k and v, float16 or bfloat16, of the same shape and strides, the last dimension
+    contiguous.  Token-major pages are the transposed view of a [pages][page][heads][dim] tensor."""
+
+    def __init__(self, k, v):
+        code = spear._dtype_code(k)
+        _require(k.dim() in (4, 5), f"k must be [pages][heads][page][dim] or have a leading layer "
+                                    f"dimension, got {k.dim()}-D")
+        _require(k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype,
+                 "k and v must agree in shape, strides and dtype")
+        _require(k.device == v.device, f"k is on {k.device}, v on {v.device}")
+        _require(k.numel() > 0, "the cache is empty")
+        _require(k.stride(-1) == 1, "the last dimension of the cache must be contiguous")
+        shape, strides = tuple(k.shape), k.stride()
+        if k.dim() == 4:
+            shape, strides = (1,) + shape, (0,) + strides
+        _require(max(shape) < 2 ** 31, f"cache of shape {tuple(k.shape)} is too large")
+        self.k, self.v, self.device = k, v, k.device
+        self.n_layers, self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = shape
+        self.c = SpearKVCacheC(k.data_ptr(), v.data_ptr(), code, *shape, *strides[:4])
+        self.ref = ctypes.byref(self.c)
+
+    def layer(self, i: int) -> "SpearKVCache":
+        """The cache of layer i, for the attention and append calls."""
+        _require(self.k.dim() == 5, "the cache has no layer dimension")
+        return SpearKVCache(self.k[i], self.v[i])
+
+
+class SpearKVBatch:
+    """The sequences of one step (int32 device tensors): block_table [seqs][width], kv_lens [seqs]
+    with the step's tokens included, q_starts [seqs + 1] or None for one token each."""
+
+    def __init__(self, block_table, kv_lens, q_starts=None):
+        _int32(block_table, "block_table", 2)
+        self.device = block_table.device
+        _int32(kv_lens, "kv_lens", 1, self.device)
+        n, width = block_table.shape
+        _require(kv_lens.numel() == n, f"kv_lens has {kv_lens.numel()} entries, block_table {n} rows")
+        _require(width >= 1, "block_table has no columns")
+        if q_starts is not None:
+            _int32(q_starts, "q_starts", 1, self.device)
+            _require(q_starts.numel() == n + 1, f"q_starts has {q_starts.numel()} entries, expected {n + 1}")
+        self.block_table, self.kv_lens, self.q_starts = block_table, kv_lens, q_starts
+        self.n_seqs = n
+        self.c = SpearKVBatchC(n, width, n, block_table.data_ptr(), kv_lens.data_ptr(),
+                               None if q_starts is None else q_starts.data_ptr())
+
+    def rows(self, n_tokens: int):
+        """The C struct for a call with this many rows."""
+        if n_tokens == self.c.n_tokens:
+            return ctypes.byref(self.c)
+        c = SpearKVBatchC.from_buffer_copy(self.c)
+        c.n_tokens = n_tokens
+        return ctypes.byref(c)
+
+
+class SpearKVPool:
+    """The pages' bookkeeping (int32 device tensors): refs [pages], table [slots][width], lens
+    [slots]; see spear_kv_pool_t.  Allocates its scratch."""
+
+    def __init__(self, refs, table, lens, page_size: int):
+        import torch
+        _int32(refs, "refs", 1)
+        self.device = refs.device
+        _int32(table, "table", 2, self.device)
+        _int32(lens, "lens", 1, self.device)
+        _require(lens.numel() == table.shape[0], f"lens has {lens.numel()} entries, table {table.shape[0]} rows")
+        _require(refs.numel() > 0 and table.numel() > 0, "the pool is empty")
+        n_slots, width = table.shape
+        words = int(load_library().spear_kv_scratch_words(refs.numel(), n_slots, width))
+        if words == 0:
+            raise SpearError(SPEAR_ERR_INVALID_ARGUMENT, "invalid pool sizes")
+        self.refs, self.table, self.lens, self.page_size = refs, table, lens, int(page_size)
+        self.scratch = torch.empty(words, dtype=torch.int32, device=self.device)
+        self.c = SpearKVPoolC(refs.numel(), self.page_size, n_slots, width, refs.data_ptr(),
+                              table.data_ptr(), lens.data_ptr(), self.scratch.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+    @classmethod
+    def new(cls, num_pages: int, page_size: int, n_slots: int, table_width: int, device="cuda"):
+        """A pool whose pages are all free."""
+        import torch
+        return cls(torch.zeros(num_pages, dtype=torch.int32, device=device),
+                   torch.full((n_slots, table_width), -1, dtype=torch.int32, device=device),
+                   torch.zeros(n_slots, dtype=torch.int32, device=device), page_size)
+
+
+def spear_attn_workspace_bytes(cache: SpearKVCache, n_q_heads: int, n_seqs: int, n_tokens: int) -> int:
+    return int(load_library().spear_attn_workspace_bytes(cache.ref, int(n_q_heads), int(n_seqs),
+                                                         int(n_tokens)))
+
+
+def new_attn_workspace(cache: SpearKVCache, n_q_heads: int, n_seqs: int, n_tokens: int):
+    """A zeroed, 256-byte aligned workspace for attention calls of at most these sizes."""
+    import torch
+    n = spear_attn_workspace_bytes(cache, n_q_heads, n_seqs, n_tokens)
+    if n == 0:
+        raise SpearError(SPEAR_ERR_INVALID_ARGUMENT, spear.spear_last_error())
+    buf = torch.zeros(n + 256, dtype=torch.uint8, device=cache.device)
+    off = (-buf.data_ptr()) % 256
+    return buf[off:off + n]
+
+
+def _rows(t, name: str, cache, tokens=None, heads=None) -> None:
+    """t is [tokens][heads][head_dim] of the cache's dtype, its last dimension contiguous."""
+    _require(t.dim() == 3, f"{name} must be [tokens][heads][head_dim], got {t.dim()}-D")
+    _require(t.dtype == cache.k.dtype, f"{name} has dtype {t.dtype}, the cache {cache.k.dtype}", TypeError)
+    shape = t.shape
+    _require(shape[2] == cache.head_dim and (tokens is None or shape[0] == tokens)
+             and (heads is None or shape[1] == heads),
+             f"{name} has shape {tuple(shape)}, expected "
+             f"({'any' if tokens is None else tokens}, {'any' if heads is None else heads}, {cache.head_dim})")
+    _require(t.stride(2) == 1, f"the last dimension of {name} must be contiguous")
+    _require(t.device == cache.device, f"{name} is on {t.device}, the cache on {cache.device}")
+
+
+def _overlap(a, b) -> bool:
+    """Whether the address ranges of two tensors meet."""
+    def span(t):
+        return t.data_ptr(), t.data_ptr() + t.element_size() * (
+            1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+def _attention(fn, cache, batch, q, out, scale, window, sinks, workspace, return_lse, stream, decode):
+    import torch
+    _rows(q, "q", cache)
+    T, Hq, D = q.shape
+    _require(batch.device == cache.device, f"the batch is on {batch.device}, the cache on {cache.device}")
+    if batch.q_starts is None:
+        _require(T == batch.n_seqs, f"q has {T} rows for {batch.n_seqs} sequences of one token")
+    else:
+        _require(not decode, "decode takes one token per sequence: the batch has q_starts")
+    if out is not None:
+        _rows(out, "out", cache, T, Hq)
+        _require(not _overlap(out, q), "out must not overlap q")
+        _require(not _overlap(out, cache.k) and not _overlap(out, cache.v),
+                 "out must not overlap the cache")
+    if workspace is not None:
+        _require(workspace.is_contiguous() and workspace.device == cache.device,
+                 f"workspace must be contiguous and on {cache.device}")
+    _gpu(cache.device)
+    on = _On(cache.device, stream)
+    made = []
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=cache.device)
+        made.append(out)
+    lse = None
+    if return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=cache.device)
+        made.append(lse)
+    if made:
+        on.made(*made)
+    args = SpearAttnArgsC(Hq, window, sinks, 1.0 / math.sqrt(D) if scale is None else scale,
+                          q.data_ptr(), q.stride(0), q.stride(1),
+                          out.data_ptr(), out.stride(0), out.stride(1),
+                          None if lse is None else lse.data_ptr())
+    ws, ws_bytes = (None, 0) if workspace is None else \
+        (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    with on as ptr:
+        _check(fn(cache.ref, batch.rows(T), ctypes.byref(args), ws, ws_bytes, ptr))
+    return (out, lse) if return_lse else out
+
+
+def spear_attn_decode(cache: SpearKVCache, batch: SpearKVBatch, q, out=None, scale=None,
+                      window: int = 0, sinks: int = 0, workspace=None, return_lse: bool = False,
+                      stream=None):
+    """q [seqs][heads][dim] -> out of the same shape (and lse [seqs][heads] when asked for).
+    scale None: 1 / sqrt(dim).  window 0: none."""
+    return _attention(load_library().spear_attn_decode, cache, batch, q, out, scale, window, sinks,
+                      workspace, return_lse, stream, True)
+
+
+def spear_attn_prefill(cache: SpearKVCache, batch: SpearKVBatch, q, out=None, scale=None,
+                       window: int = 0, sinks: int = 0, workspace=None, return_lse: bool = False,
+                       stream=None):
+    """q [tokens][heads][dim], rows as in the batch's q_starts -> out of the same shape."""
+    return _attention(load_library().spear_attn_prefill, cache, batch, q, out, scale, window, sinks,
+                      workspace, return_lse, stream, False)
+
+
+def spear_kv_append(cache: SpearKVCache, batch: SpearKVBatch, k, v, stream=None) -> None:
+    """Store new keys and values [tokens][kv heads][dim] in the batch's pages."""
+    _rows(k, "k", cache, heads=cache.n_kv_heads)
+    T = k.shape[0]
+    _rows(v, "v", cache, T, cache.n_kv_heads)
+    _require(batch.device == cache.device, f"the batch is on {batch.device}, the cache on {cache.device}")
+    _require(batch.q_starts is not None or T == batch.n_seqs,
+             f"k has {T} rows for {batch.n_seqs} sequences of one token")
+    for new in (k, v):
+        for old in (cache.k, cache.v):
+            _require(not _overlap(new, old), "k and v must not overlap the cache")
+    _gpu(cache.device)
+    with _On(cache.device, stream) as ptr:
+        _check(load_library().spear_kv_append(
+            cache.ref, batch.rows(T), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+            v.stride(0), v.stride(1), ptr))
+
+
+def spear_kv_copy_pages(cache: SpearKVCache, src, dst, stream=None) -> None:
+    """Page src[i] to page dst[i] of all layers (int32 device tensors)."""
+    _int32(src, "src", 1, cache.device)
+    _int32(dst, "dst", 1, cache.device)
+    _require(src.numel() == dst.numel(), f"src has {src.numel()} entries, dst {dst.numel()}")
+    _gpu(cache.device)
+    with _On(cache.device, stream) as ptr:
+        _check(load_library().spear_kv_copy_pages(cache.ref, src.data_ptr(), dst.data_ptr(),
+                                                  src.numel(), ptr))
+
+
+def spear_kv_fork(pool: SpearKVPool, src, dst, stream=None) -> None:
+    """Slots dst[i] become copies of slots src[i] that share their pages."""
+    _int32(src, "src", 1, pool.device)
+    _int32(dst, "dst", 1, pool.device)
+    _require(src.numel() == dst.numel(), f"src has {src.numel()} entries, dst {dst.numel()}")
+    _gpu(pool.device)
+    with _On(pool.device, stream) as ptr:
+        _check(load_library().spear_kv_fork(pool.ref, src.data_ptr(), dst.data_ptr(), src.numel(), ptr))
+
+
+def spear_kv_reserve(pool: SpearKVPool, cache: SpearKVCache, slots, new_lens, missing=None,
+                     stream=None):
+    """Pages for slots to hold new_lens tokens, copy on write -> missing, an int32 device tensor
+    [1]: 0, or how many pages lack (then nothing was changed), or -1 for an invalid entry."""
+    import torch
+    _int32(slots, "slots", 1, pool.device)
+    _int32(new_lens, "new_lens", 1, pool.device)
+    _require(slots.numel() == new_lens.numel(), f"slots has {slots.numel()} entries, new_lens {new_lens.numel()}")
+    _require(cache.device == pool.device, f"the cache is on {cache.device}, the pool on {pool.device}")
+    if missing is not None:
+        _int32(missing, "missing", 1, pool.device)
+        _require(missing.numel() == 1, "missing must hold one value")
+    _gpu(pool.device)
+    on = _On(pool.device, stream)
+    if missing is None:
+        missing = torch.empty(1, dtype=torch.int32, device=pool.device)
+        on.made(missing)
+    with on as ptr:
+        _check(load_library().spear_kv_reserve(pool.ref, cache.ref, slots.data_ptr(),
+                                               new_lens.data_ptr(), slots.numel(),
+                                               missing.data_ptr(), ptr))
+    return missing
+
+
+def spear_kv_free(pool: SpearKVPool, slots, stream=None) -> None:
+    """Release the pages of slots."""
+    _int32(slots, "slots", 1, pool.device)
+    _gpu(pool.device)
+    with _On(pool.device, stream) as ptr:
+        _check(load_library().spear_kv_free(pool.ref, slots.data_ptr(), slots.numel(), ptr))
+
+
+def spear_kv_compact(pool: SpearKVPool, cache: SpearKVCache, used=None, stream=None):
+    """Move the used pages to the lowest indices -> used, an int32 device tensor [1]: how many."""
+    import torch
+    _require(cache.device == pool.device, f"the cache is on {cache.device}, the pool on {pool.device}")
+    if used is not None:
+        _int32(used, "used", 1, pool.device)
+        _require(used.numel() == 1, "used must hold one value")
+    _gpu(pool.device)
+    on = _On(pool.device, stream)
+    if used is None:
+        used = torch.empty(1, dtype=torch.int32, device=pool.device)
+        on.made(used)
+    with on as ptr:
+        _check(load_library().spear_kv_compact(pool.ref, cache.ref, used.data_ptr(), ptr))
+    return used

@@ -9,6 +9,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "attn_internal.h"
 #include "internal.h"
 
 using namespace spear;
@@ -229,6 +230,14 @@ spear_status_t noalloc_scratch(hipStream_t stream, void **out) {
 }
 
 }  // namespace
+
+namespace spear {
+
+spear_status_t set_last_error(spear_status_t st, const char *text) {
+  return st == SPEAR_OK ? ok() : fail(st, "%s", text);
+}
+
+}  // namespace spear
 
 extern "C" {
 
