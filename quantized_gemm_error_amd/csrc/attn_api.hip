@@ -94,6 +94,9 @@ spear_status_t check_batch(const spear_kv_batch_t *b, int page_size) {
   if ((int64_t)b->table_width * page_size > (int64_t(1) << 30))
     return fail(SPEAR_ERR_UNSUPPORTED, "table_width=%d pages of %d tokens exceed 2^30 tokens",
                 b->table_width, page_size);
+  if ((int64_t)b->n_seqs * b->table_width * page_size > (int64_t(1) << 35))
+    return fail(SPEAR_ERR_UNSUPPORTED, "block_table of %d x %d pages of %d tokens exceeds 2^35 tokens",
+                b->n_seqs, b->table_width, page_size);
   if (!b->q_starts && b->n_tokens != b->n_seqs)
     return fail(SPEAR_ERR_INVALID_ARGUMENT, "without q_starts n_tokens=%d must equal n_seqs=%d",
                 b->n_tokens, b->n_seqs);

@@ -26,4 +26,66 @@ __device__ __forceinline__ int cached_len(const AttnDesc &d, int b) {
   return max(0, min(d.kv_lens[b], d.width * d.page_size));
 }
 
+// Scores are kept times log2(e), so that the softmax is in powers of two; a
+// row's maximum starts at a finite value, below any score that counts, so
+// that a score of -infinity (a hidden key) weighs exactly 0.
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -1e30f;
+
+// Every lane gets op over its own value and the values of the lanes 16 and
+// 32 places away: the four lanes that hold one column of a 16-wide MFMA.
+// (permlane swaps of a register with itself put both halves side by side.)
+template <typename Op>
+__device__ __forceinline__ float over_columns(float v, Op op) {
+  const uint32_t u = bitcast<uint32_t>(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const float w = op(bitcast<float>((uint32_t)a[0]), bitcast<float>((uint32_t)a[1]));
+  const uint32_t x = bitcast<uint32_t>(w);
+  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return op(bitcast<float>((uint32_t)b[0]), bitcast<float>((uint32_t)b[1]));
+}
+__device__ __forceinline__ float columns_max(float v) {
+  return over_columns(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float columns_sum(float v) {
+  return over_columns(v, [](float a, float b) { return a + b; });
+}
+
+// Inclusive prefix sum over a wave, in six adds with shifted operands.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31
+  return v;
+}
+__device__ __forceinline__ int wave_total(int v) {
+  return __builtin_amdgcn_readlane(wave_scan(v), 63);
+}
+
+// Two fp32 values rounded to nearest even into a packed pair.
+template <int DT>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+  if constexpr (DT == DT_F16) {
+    return bitcast<uint32_t>(f16x2_t{(_Float16)a, (_Float16)b});
+  } else {
+    return bitcast<uint32_t>(bf16x2_t{(__bf16)a, (__bf16)b});
+  }
+}
+
+// Read-only words at wave-uniform addresses, through the scalar cache: their
+// wait (lgkmcnt) does not drain the vector loads in flight.
+typedef const __attribute__((address_space(4))) int32_t *scalar_i32;
+__device__ __forceinline__ int scalar_load(const int32_t *p, int64_t i) {
+  return ((scalar_i32)(uintptr_t)p)[i];
+}
+
+// The header of an attention workspace: counters that every call leaves at
+// zero, at the same place for calls of any size.  The data that a call
+// writes before it reads it lies past it.
+constexpr int kAttnCounters = 65536;
+constexpr size_t kAttnDataOff = kAttnCounters * sizeof(uint32_t);
+
 }  // namespace spear
