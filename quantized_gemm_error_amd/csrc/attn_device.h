@@ -85,7 +85,7 @@ __device__ __forceinline__ int scalar_load(const int32_t *p, int64_t i) {
 // The header of an attention workspace: counters that every call leaves at
 // zero, at the same place for calls of any size.  The data that a call
 // writes before it reads it lies past it.
-constexpr int kAttnCounters = 65536;
+constexpr int kAttnCounters = 4096;
 constexpr size_t kAttnDataOff = kAttnCounters * sizeof(uint32_t);
 
 }  // namespace spear
