@@ -128,6 +128,8 @@ spear_status_t attention(const spear_kv_cache_t *c, const spear_kv_batch_t *b,
   if (a->n_q_heads < 1 || a->n_q_heads % c->n_kv_heads != 0)
     return fail(SPEAR_ERR_INVALID_ARGUMENT, "n_q_heads=%d is not a multiple of n_kv_heads=%d",
                 a->n_q_heads, c->n_kv_heads);
+  if ((int64_t)b->n_tokens * a->n_q_heads > (int64_t(1) << 30))
+    return fail(SPEAR_ERR_UNSUPPORTED, "n_tokens=%d rows of n_q_heads=%d exceed 2^30", b->n_tokens, a->n_q_heads);
   if (a->n_q_heads > 4096) return fail(SPEAR_ERR_UNSUPPORTED, "n_q_heads=%d exceeds 4096", a->n_q_heads);
   if (a->window < 0 || a->sinks < 0)
     return fail(SPEAR_ERR_INVALID_ARGUMENT, "window=%d and sinks=%d must be >= 0", a->window, a->sinks);

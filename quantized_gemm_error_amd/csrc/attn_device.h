@@ -75,6 +75,61 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
   }
 }
 
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// D = A * B + C for one 32x32x16 block.  Lane l supplies row l % 32 of A and
+// column l % 32 of B, eight contraction places of half l / 32 each.  D lands
+// as rows 8 * (v / 4) + 4 * (l / 32) + v % 4, column l % 32, v = 0..15.
+template <int DT>
+__device__ __forceinline__ f32x16_t mfma_32x32x16(u32x4_t a, u32x4_t b, f32x16_t c) {
+  if constexpr (DT == DT_F16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(bitcast<f16x8_t>(a), bitcast<f16x8_t>(b), c, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(bitcast<bf16x8_t>(a), bitcast<bf16x8_t>(b), c, 0, 0, 0);
+  }
+}
+
+// op over a lane's value and that of the lane 32 places away.
+template <typename Op>
+__device__ __forceinline__ float over_halves(float v, Op op) {
+  const uint32_t u = bitcast<uint32_t>(v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return op(bitcast<float>((uint32_t)a[0]), bitcast<float>((uint32_t)a[1]));
+}
+
+// Pairs of the type's exponent bits, and one of each: a half of
+// (x & kExp) + kExpOne has its top bit set where x is infinite or no number.
+template <int DT>
+constexpr uint32_t kExp = DT == DT_F16 ? 0x7C007C00u : 0x7F807F80u;
+template <int DT>
+constexpr uint32_t kExpOne = DT == DT_F16 ? 0x04000400u : 0x00800080u;
+template <int DT>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  return ((x & kExp<DT>) + kExpOne<DT>) & 0x80008000u;
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A buffer of `bytes` bytes at p, both wave-uniform, as its descriptor words.
+__device__ __forceinline__ u32x4_t buffer_words(const void *p, int bytes) {
+  const uint64_t a = (uint64_t)p;
+  return u32x4_t{(uint32_t)uniform((int)a), (uint32_t)uniform((int)(a >> 32)) & 0xFFFFu,
+                 (uint32_t)uniform(bytes), 0x00020000u};
+}
+
+// 16 bytes per lane from a buffer to LDS: lane i's go to LDS byte lds + 16 i.
+// Bytes past the buffer's range read as zeros.  Written out because the
+// compiler waits for every such load before any later LDS read; the caller
+// waits (vmcnt) before a barrier instead.  It writes no register but m0, which
+// needs one wait state before the load reads it and is used by nothing else
+// in these kernels.
+__device__ __forceinline__ void load_to_lds(u32x4_t buffer, uint32_t lds, int byte_off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(byte_off), "s"(buffer)
+               : "memory");
+}
+
 // Read-only words at wave-uniform addresses, through the scalar cache: their
 // wait (lgkmcnt) does not drain the vector loads in flight.
 typedef const __attribute__((address_space(4))) int32_t *scalar_i32;
