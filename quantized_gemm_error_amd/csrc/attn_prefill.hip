@@ -1,6 +1,6 @@
 // Causal attention of the batch's new tokens over the paged cache.
 //
-// With s = q . k log2(e) scale, tiles of 64 keys pass by a block of query rows
+// With s = q . k scale log2(e), tiles of 64 keys pass by a block of query rows
 // that keeps a reference m >= (row maximum) - 8, l = sum 2^(s - m) and
 // o = sum 2^(s - m) v in fp32 (m is raised, and l and o scaled, only when a
 // maximum passes it by more than 8: the weights stay below 2^8, and their
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   constexpr int RPI = 64 / CH;       // rows a wave's load instruction brings
   constexpr int LOADS = 16 / RPI;    // instructions for 16 keys
   constexpr int TILE = kKeys * D * 2;  // bytes of a staged K or V tile
-  __shared__ __attribute__((aligned(256))) char s_kv[2][2][TILE];
+  __shared__ __attribute__((aligned(256))) char s_kv[4][TILE];  // K tiles of even and odd t, then V's
   __shared__ uint32_t s_weights[D == 64 ? kWaves * 16 * 64 : 1];  // (slow path; D = 128: the K tile)
   __shared__ int s_dirty[2][kWaves];
 
@@ -144,8 +144,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   {
     const uint16_t *from = d.q + (int64_t)(blk.start + tok) * d.q_tok + head * d.q_head + 8 * half;
 #pragma unroll
-    for (int k = 0; k < KS; ++k) q[k] = *(const u32x4_t *)(from + 16 * k);
+    for (int k = 0; k < KS; ++k) {
+      q[k] = *(const u32x4_t *)(from + 16 * k);
+      if (d.scale < 0.f) q[k] ^= 0x80008000u;
+    }
   }
+  // scores stay unscaled (a negative scale has turned the query's sign): the
+  // weight is 2^(s scale - m scale), one fma
+  const float scale = fmaxf(fabsf(d.scale) * kLog2e, 1e-30f), slack = kSlack / scale;
 
   // staging: this wave's 16 keys of a tile
   int k_src[LOADS], v_src[LOADS];  // byte offsets from the first key
@@ -161,181 +167,199 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
     const int page = i < halves ? uniform(scalar_load(d.table, (int64_t)blk.b * d.width + i / p16)) : -1;
     return (uint32_t)page < (uint32_t)d.num_pages ? page : -1;
   };
-  // Starts the loads of the tile at key0; which of its groups are hidden.
-  const auto stage = [&](int key0, int buf) {
-    int pages[kKeys / 16], hidden = 0, mine = -1;
+  // Where this wave's 16 keys of the tile at key0 lie; which of the tile's
+  // groups are hidden.
+  struct Source {
+    int64_t off;
+    int bytes, hidden;
+  };
+  const auto source_of = [&](int key0) {
+    Source src;
+    int mine = -1;
+    src.hidden = 0;
 #pragma unroll
     for (int u = 0; u < kKeys / 16; ++u) {
-      pages[u] = page_of(key0 / 16 + u);
-      hidden |= (pages[u] < 0) << u;
-      if (u == wave) mine = pages[u];
+      const int page = page_of(key0 / 16 + u);
+      src.hidden |= (page < 0) << u;
+      if (u == wave) mine = page;
     }
     const int i = key0 / 16 + wave;
-    const int64_t off = max(mine, 0) * d.s_page + (int64_t)kvh * d.s_head +
-                        (int64_t)(i % p16) * 16 * d.s_token;
-    const int bytes = mine < 0 ? 0 : max(0, min(16, len - 16 * i)) * 2 * (int)d.s_token;
-    const u32x4_t kr = buffer_words(d.k + off, bytes), vr = buffer_words(d.v + off, bytes);
+    src.off = max(mine, 0) * d.s_page + (int64_t)kvh * d.s_head + (int64_t)(i % p16) * 16 * d.s_token;
+    src.bytes = mine < 0 ? 0 : max(0, min(16, len - 16 * i)) * 2 * (int)d.s_token;
+    return src;
+  };
+  const uint32_t lds = lds_offset(s_kv), mine_at = 16 * wave * D * 2;
+  const auto load_tile = [&](const uint16_t *base, const Source &src, uint32_t to, const int *from) {
+    const u32x4_t r = buffer_words(base + src.off, src.bytes);
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      const int at = (16 * wave + j * RPI) * D * 2;
-      load_to_lds(kr, (uint32_t)uniform((int)(lds_offset(s_kv[buf][0]) + at)), k_src[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      const int at = (16 * wave + j * RPI) * D * 2;
-      load_to_lds(vr, (uint32_t)uniform((int)(lds_offset(s_kv[buf][1]) + at)), v_src[j]);
-    }
-    return hidden;
+    for (int j = 0; j < LOADS; ++j)
+      load_to_lds(r, (uint32_t)uniform((int)(to + mine_at + j * RPI * D * 2)), from[j]);
   };
 
-  // operand addresses in a tile: K row `col`, step k; V row 4 half + l/4 % 4, dim block b
-  int k_at[KS], v_at[DB];
-#pragma unroll
-  for (int k = 0; k < KS; ++k) k_at[k] = col * D * 2 + 16 * ((2 * k) ^ (half ^ (col & (CH - 1))));
-  {
-    const int i = lane & 15, sub = (lane >> 4) & 1;
-#pragma unroll
-    for (int b = 0; b < DB; ++b)
-      v_at[b] = (4 * half + (i >> 2)) * D * 2 + 32 * ((2 * b + sub) ^ v_swizzle<D>(i >> 2)) + 8 * (i & 3);
-  }
+  // operand addresses in a tile: K row `col`, step 0 (step k: ^ 32 k); V row
+  // 4 half + l/4 % 4, dim block 0 (block b: ^ 64 b)
+  const int k_at = col * D * 2 + 16 * (half ^ (col & (CH - 1)));
+  const int v_at = (4 * half + ((lane & 15) >> 2)) * D * 2 +
+                   32 * (((lane >> 4) & 1) ^ v_swizzle<D>((lane & 15) >> 2)) + 8 * (lane & 3);
 
-  f32x16_t acc[DB];
+  f32x16_t acc[DB], s[2];
 #pragma unroll
   for (int b = 0; b < DB; ++b)
 #pragma unroll
     for (int v = 0; v < 16; ++v) acc[b][v] = 0.f;
   float m = kNoMax, l = 0.f;
-  const float scale = d.scale * kLog2e;
   const int window = d.window > 0 ? d.window : 0x7FFFFFFF;
   // whether some row of positions first..last does not see all of a tile
   const auto partly = [&](int key0, int first, int last) {
-    return key0 + kKeys - 1 > first || (d.window > 0 && last - key0 >= d.window && key0 + kKeys > d.sinks);
+    return key0 + kKeys - 1 > first || (last - key0 >= window && key0 + kKeys > d.sinks);
+  };
+  // scores of a tile's keys 32 u .. 32 u + 31
+  const auto scores = [&](const char *kt, int u) {
+    f32x16_t c;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) c[v] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+      c = mfma_32x32x16<DT>(*(const u32x4_t *)(kt + (k_at ^ (32 * k)) + u * 32 * D * 2), q[k], c);
+    return c;
   };
 
-  int hidden_next = tiles > 0 ? stage(key_of(0), 0) : 0;
-  for (int t = 0; t < tiles; ++t) {
-    const int buf = t & 1, key0 = key_of(t), hidden = hidden_next;
-    const bool masked = partly(key0, p_min, p_max);
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the tile is in LDS
-    if (masked) {  // (only V: a score that is no number is replaced, a weight of 0 is not)
-      uint32_t bad = 0;
-#pragma unroll
-      for (int j = 0; j < LOADS; ++j) {
-        const u32x4_t x = *(const u32x4_t *)(s_kv[buf][1] + (16 * wave + j * RPI) * D * 2 + 16 * lane);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) bad |= not_finite<DT>(x[e]);
-      }
-      const bool any = __any(bad != 0);
-      if (lane == 0) s_dirty[buf][wave] = any;
-    }
+  // The tiles that some row of this wave sees are the first w_tiles (those
+  // that a window hides from all of its rows are computed and masked).
+  const int w_tiles = !active || w_max < 0 ? 0 : min(tiles, tiles - (p_max / kKeys - w_max / kKeys));
+  if (tiles > 0) {
+    Source now = source_of(key_of(0)), next = now;
+    load_tile(d.k, now, lds, k_src);
+    __builtin_amdgcn_s_waitcnt(0x0F70);
     lds_barrier();
-    if (t + 1 < tiles) hidden_next = stage(key_of(t + 1), buf ^ 1);
-    const bool dirty = masked && (s_dirty[buf][0] | s_dirty[buf][1] | s_dirty[buf][2] | s_dirty[buf][3]);
-    // (rows of a wave may all lie before the tile, or all past its window)
-    const bool unseen = !active || key0 > w_max ||
-                        (d.window > 0 && w_min - (key0 + kKeys - 1) >= d.window && key0 >= d.sinks);
-    if (unseen && !dirty) continue;
-
-    f32x16_t s[2];
-    const char *kt = s_kv[buf][0];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int v = 0; v < 16; ++v) s[u][v] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-        s[u] = mfma_32x32x16<DT>(*(const u32x4_t *)(kt + k_at[k] + u * 32 * D * 2), q[k], s[u]);
+    load_tile(d.v, now, lds + 2 * TILE, v_src);
+    if (tiles > 1) {
+      next = source_of(key_of(1));
+      load_tile(d.k, next, lds + TILE, k_src);
     }
+    if (w_tiles > 0) {
+      s[0] = scores(s_kv[0], 0);
+      s[1] = scores(s_kv[0], 1);
+    }
+    for (int t = 0; t < tiles; ++t) {
+      // here: s holds tile t's scores; V of t and K of t + 1 are on their way
+      const int buf = t & 1, key0 = key_of(t), hidden = now.hidden;
+      const char *kt = s_kv[buf ^ 1], *vt = s_kv[2 + buf];
+      const bool masked = partly(key0, p_min, p_max);
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's parts are in LDS
+      if (masked) {  // (only V: a score that is no number is replaced, a weight of 0 is not)
+        bool any = false;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+        for (int j = 0; j < LOADS; ++j) {
+          u32x4_t *at = (u32x4_t *)(s_kv[2 + buf] + mine_at + j * RPI * D * 2 + 16 * lane);
+          u32x4_t x = *at;
+          uint32_t bad = 0;
 #pragma unroll
-      for (int v = 0; v < 16; ++v) s[u][v] *= scale;
-    if (hidden || partly(key0, w_min, w_max) || !is_row) {
+          for (int e = 0; e < 4; ++e) bad |= not_finite<DT>(x[e]);
+          if (__any(bad != 0)) {  // left out of the products, added below
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] &= ~((not_finite<DT>(x[e]) >> 15) * 0xFFFFu);
+            *at = x;
+            any = true;
+          }
+        }
+        if (lane == 0) s_dirty[buf][wave] = any;
+      }
+      lds_barrier();
+      now = next;
+      if (t + 1 < tiles) load_tile(d.v, now, lds + (2 + (buf ^ 1)) * TILE, v_src);
+      if (t + 2 < tiles) {
+        next = source_of(key_of(t + 2));
+        load_tile(d.k, next, lds + buf * TILE, k_src);
+      }
+      const bool dirty = masked && (s_dirty[buf][0] | s_dirty[buf][1] | s_dirty[buf][2] | s_dirty[buf][3]);
+      const bool mine = t < w_tiles;
+      if (!mine && !dirty) continue;
+
+      if (hidden || partly(key0, w_min, w_max) || !is_row) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int j = key0 + 32 * u + 8 * (v >> 2) + 4 * half + (v & 3);
+            const bool sees = (j <= pos) & ((pos - j < window) | (j < d.sinks)) &
+                              (((hidden >> (2 * u + (v >> 3))) & 1) == 0);
+            s[u][v] = sees ? s[u][v] : -INFINITY;
+          }
+      }
+      float top = s[0][0];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int j = key0 + 32 * u + 8 * (v >> 2) + 4 * half + (v & 3);
-          const bool sees = (j <= pos) & ((pos - j < window) | (j < d.sinks)) &
-                            (((hidden >> (2 * u + (v >> 3))) & 1) == 0);
-          s[u][v] = sees ? s[u][v] : -INFINITY;
-        }
-    }
-    float top = s[0][0];
+        for (int v = 0; v < 16; ++v) top = fmaxf(top, s[u][v]);
+      if (__any(top > m + slack)) {
+        top = over_halves(top, [](float a, float b) { return fmaxf(a, b); });
+        const float m2 = fmaxf(m, top), f = __builtin_amdgcn_exp2f((m - m2) * scale);
+        m = m2;
+        l *= f;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+        for (int b = 0; b < DB; ++b)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) top = fmaxf(top, s[u][v]);
-    if (__any(top > m + kSlack)) {
-      top = over_halves(top, [](float a, float b) { return fmaxf(a, b); });
-      const float m2 = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - m2);
-      m = m2;
-      l *= f;
-#pragma unroll
-      for (int b = 0; b < DB; ++b)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[b][v] *= f;
-    }
-    u32x4_t p[4];  // weights of 16 keys each, as the column operand of O
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int v = 0; v < 16; v += 2) {
-        const float a = __builtin_amdgcn_exp2f(s[u][v] - m), b = __builtin_amdgcn_exp2f(s[u][v + 1] - m);
-        l += a + b;
-        p[2 * u + (v >> 3)][(v >> 1) & 3] = pack_pair<DT>(a, b);
+          for (int v = 0; v < 16; ++v) acc[b][v] *= f;
       }
-    const char *vt = s_kv[buf][1];
-    const auto add_values = [&](auto sanitize) {
+      // the weights of 16 keys each, as the column operand of O; meanwhile the
+      // matrix unit forms the next tile's scores
+      u32x4_t p[4];
+      const float shift = -m * scale;
+      f32x16_t ahead[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        ahead[u] = scores(kt, u);
+#pragma unroll
+        for (int v = 0; v < 16; v += 2) {
+          const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][v], scale, shift));
+          const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][v + 1], scale, shift));
+          l += a + b;
+          p[2 * u + (v >> 3)][(v >> 1) & 3] = pack_pair<DT>(a, b);
+        }
+      }
+      s[0] = ahead[0];
+      s[1] = ahead[1];
 #pragma unroll
       for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int b = 0; b < DB; ++b) {
-          const auto x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(vt + v_at[b] + g * 16 * D * 2));
-          const auto y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(vt + v_at[b] + (g * 16 + 8) * D * 2));
-          const uint2 xu = bitcast<uint2>(x), yu = bitcast<uint2>(y);
-          u32x4_t a = {xu.x, xu.y, yu.x, yu.y};
-          if constexpr (decltype(sanitize)::value) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] &= ~((not_finite<DT>(a[e]) >> 15) * 0xFFFFu);
-          }
-          acc[b] = mfma_32x32x16<DT>(a, p[g], acc[b]);
+          const char *from = vt + (v_at ^ (64 * b)) + g * 16 * D * 2;
+          const uint2 x = bitcast<uint2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)from));
+          const uint2 y = bitcast<uint2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(from + 8 * D * 2)));
+          acc[b] = mfma_32x32x16<DT>(u32x4_t{x.x, x.y, y.x, y.y}, p[g], acc[b]);
         }
-    };
-    if (!dirty) {
-      add_values(std::false_type());
-      continue;
-    }
-    add_values(std::true_type());
-    {
-      // What the sanitized products left out: the values that are not finite,
-      // for the rows that see their keys.  Weights go through LDS (D = 128:
-      // where the K tile was, once every wave is past it), keys one by one.
+      if (!dirty) continue;
+      // Values that are not finite, key by key, for the rows that see them.
+      // The weights go through LDS (D = 128: where the K tile was, once every
+      // wave is past it), the values come from memory again.
       lds_barrier();
-      uint32_t *w_at = D == 64 ? s_weights : (uint32_t *)s_kv[buf][0];
-      w_at += wave * 16 * 64;
+      uint32_t *w_at = (D == 64 ? s_weights : (uint32_t *)kt) + wave * 16 * 64;
 #pragma unroll
       for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int e = 0; e < 4; ++e) w_at[(4 * g + e) * 64 + lane] = p[g][e];
       lds_barrier();
+      if (!mine) continue;
       for (int j = 0; j < kKeys; ++j) {
+        const int key = key0 + j, page = page_of(key / 16);
+        if (page < 0 || key >= len) continue;
         const int in16 = j & 15, e = (in16 & 3) + 4 * (in16 >> 3);
         const uint32_t pair = w_at[(4 * (j >> 4) + (e >> 1)) * 64 + col + 32 * ((in16 >> 2) & 1)];
         const float w = to_f32<DT>((uint16_t)(e & 1 ? pair >> 16 : pair));
-        const int key = key0 + j;
         const bool sees = (key <= pos) & ((pos - key < window) | (key < d.sinks));
+        const uint16_t *from = d.v + page * d.s_page + (int64_t)kvh * d.s_head +
+                               (int64_t)(key % d.page_size) * d.s_token + 4 * half;
 #pragma unroll
         for (int b = 0; b < DB; ++b)
 #pragma unroll
           for (int v4 = 0; v4 < 4; ++v4) {  // dims 32 b + 8 v4 + 4 half + 0..3
-            const int seg = (2 * b + (v4 >> 1)) ^ v_swizzle<D>(j);
-            const uint2 x = *(const uint2 *)(vt + j * D * 2 + 32 * seg + 16 * (v4 & 1) + 8 * half);
+            const uint2 x = *(const uint2 *)(from + 32 * b + 8 * v4);
 #pragma unroll
             for (int e2 = 0; e2 < 4; ++e2) {
               const uint32_t y = e2 < 2 ? x.x : x.y;
               const uint16_t bits = (uint16_t)(e2 & 1 ? y >> 16 : y);
-              if (sees && not_finite<DT>(bits)) acc[b][4 * v4 + e2] += w * to_f32<DT>(bits);
+              if (sees & (not_finite<DT>(bits) != 0)) acc[b][4 * v4 + e2] += w * to_f32<DT>(bits);
             }
           }
       }
@@ -353,7 +377,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
                                               pack_pair<DT>(acc[b][v + 2] * inv, acc[b][v + 3] * inv)};
   if (d.lse && half == 0)
     d.lse[(int64_t)(blk.start + tok) * d.Hq + head] =
-        l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+        l != 0.f ? (m * scale + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace
