@@ -159,6 +159,13 @@ spear_status_t attention(const spear_kv_cache_t *c, const spear_kv_batch_t *b,
   d.G = d.Hq / d.Hkv;
   d.page_size = c->page_size;
   d.num_pages = c->num_pages;
+  // with 2^(s-1) < p <= 2^s, mul = ceil(2^(31+s) / p) exceeds the quotient by
+  // less than one, so i mul / 2^(31+s) is less than 1 / p above i / p
+  if (const uint32_t p16 = c->page_size / 16; p16 > 1) {
+    const int sh = 32 - __builtin_clz(p16 - 1);
+    d.p16_mul = (uint32_t)(((uint64_t(1) << (31 + sh)) + p16 - 1) / p16);
+    d.p16_shift = sh - 1;
+  }
   d.k = (const uint16_t *)c->k;
   d.v = (const uint16_t *)c->v;
   d.s_page = c->stride_page;

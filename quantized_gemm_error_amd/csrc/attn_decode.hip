@@ -178,7 +178,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) void attn_decode_kernel(A
     a.key0 = real * kTile;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int i = 2 * real + u, pi = i / p16;
+      const int i = 2 * real + u, pi = column_of(d, i);
       int page = i < halves ? scalar_load(d.table, (int64_t)s.b * d.width + pi) : -1;
       if ((uint32_t)page >= (uint32_t)d.num_pages) page = -1;
       a.half[u].page = page;

@@ -21,6 +21,11 @@ __device__ __forceinline__ Seen seen_by(int p, int window, int sinks) {
   return s;
 }
 
+// The table column of the 16-token group i (< 2^31) of a sequence.
+__device__ __forceinline__ int column_of(const AttnDesc &d, int i) {
+  return d.p16_mul ? (int)(__umulhi((uint32_t)i, d.p16_mul) >> d.p16_shift) : i;
+}
+
 // Cached tokens of sequence b, within what its table row can hold.
 __device__ __forceinline__ int cached_len(const AttnDesc &d, int b) {
   return max(0, min(d.kv_lens[b], d.width * d.page_size));
@@ -117,16 +122,17 @@ __device__ __forceinline__ u32x4_t buffer_words(const void *p, int bytes) {
                  (uint32_t)uniform(bytes), 0x00020000u};
 }
 
-// 16 bytes per lane from a buffer to LDS: lane i's go to LDS byte lds + 16 i.
+// 16 bytes per lane from a buffer to LDS: lane i's, at byte_off + at, go to LDS
+// byte lds + 16 i (at and lds are wave-uniform).
 // Bytes past the buffer's range read as zeros.  Written out because the
 // compiler waits for every such load before any later LDS read; the caller
 // waits (vmcnt) before a barrier instead.  It writes no register but m0, which
 // needs one wait state before the load reads it and is used by nothing else
 // in these kernels.
-__device__ __forceinline__ void load_to_lds(u32x4_t buffer, uint32_t lds, int byte_off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+__device__ __forceinline__ void load_to_lds(u32x4_t buffer, uint32_t lds, int byte_off, int at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
-               : "s"(lds), "v"(byte_off), "s"(buffer)
+               : "s"(lds), "v"(byte_off), "s"(buffer), "s"(at)
                : "memory");
 }
 

@@ -17,6 +17,7 @@ spear_status_t set_last_error(spear_status_t st, const char *text);
 struct AttnDesc {
   int dtype, D, Hq, Hkv, G;  // G = Hq / Hkv
   int page_size, num_pages;
+  uint32_t p16_mul, p16_shift;  // i / (page_size / 16) = mulhi(i, mul) >> shift for i < 2^31; mul 0: i
   const uint16_t *k, *v;
   int64_t s_page, s_head, s_token;
   int n_seqs, width, n_tokens;

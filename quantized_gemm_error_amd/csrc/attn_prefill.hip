@@ -108,8 +108,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   constexpr int LOADS = 16 / RPI;    // instructions for 16 keys
   constexpr int TILE = kKeys * D * 2;  // bytes of a staged K or V tile
   __shared__ __attribute__((aligned(256))) char s_kv[4][TILE];  // K tiles of even and odd t, then V's
-  __shared__ uint32_t s_weights[D == 64 ? kWaves * 16 * 64 : 1];  // (slow path; D = 128: the K tile)
-  __shared__ int s_dirty[2][kWaves];
+  __shared__ __attribute__((aligned(16))) int s_flags[2][kWaves];  // of a tile's 16-key groups: 1 hidden, 2 not finite
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
@@ -153,56 +152,60 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   // weight is 2^(s scale - m scale), one fma
   const float scale = fmaxf(fabsf(d.scale) * kLog2e, 1e-30f), slack = kSlack / scale;
 
-  // staging: this wave's 16 keys of a tile
-  int k_src[LOADS], v_src[LOADS];  // byte offsets from the first key
+  // Staging this wave's 16 keys of a tile: load j brings the RPI rows from
+  // j RPI on, this lane the chunk that belongs where its bytes land.  The
+  // chunks of K's row t are permuted by ^ (t & 7), which depends on j's parity
+  // (D = 128) or not on j (D = 64); V's by row alone.
+  const int lane_row = lane / CH, lane_ch = lane % CH;
+  const int row_bytes = 2 * (int)d.s_token;
+  int k_src[D == 128 ? 2 : 1];  // byte offsets from the load's first row
 #pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    const int t = i * RPI + lane / CH, c = lane % CH;
-    k_src[i] = 2 * (t * (int)d.s_token + 8 * (c ^ (t & (CH - 1))));
-    v_src[i] = 2 * (t * (int)d.s_token + 8 * ((((c >> 1) ^ v_swizzle<D>(t)) << 1) | (c & 1)));
-  }
-  const int p16 = d.page_size / 16, halves = d.width * p16;
-  // page of 16-key group i of the sequence, -1 where there is none
-  const auto page_of = [&](int i) {
-    const int page = i < halves ? uniform(scalar_load(d.table, (int64_t)blk.b * d.width + i / p16)) : -1;
-    return (uint32_t)page < (uint32_t)d.num_pages ? page : -1;
-  };
-  // Where this wave's 16 keys of the tile at key0 lie; which of the tile's
-  // groups are hidden.
+  for (int j = 0; j < (D == 128 ? 2 : 1); ++j)
+    k_src[j] = lane_row * row_bytes + 16 * (lane_ch ^ ((j * RPI + lane_row) & 7));
+  const int v_src = lane_row * row_bytes +
+                    16 * ((((lane_ch >> 1) ^ v_swizzle<D>(lane_row)) << 1) | (lane_ch & 1));
+  // Where this wave's 16 keys of the tile at key0 lie; bytes 0: nowhere.
   struct Source {
     int64_t off;
-    int bytes, hidden;
+    int bytes;
+    bool hidden;  // in the cached length, but on no page
   };
+  const int p16 = d.page_size / 16;
+  const int32_t *row_table = d.table + (int64_t)blk.b * d.width;
+  const int64_t head_off = (int64_t)kvh * d.s_head;
   const auto source_of = [&](int key0) {
     Source src;
-    int mine = -1;
-    src.hidden = 0;
-#pragma unroll
-    for (int u = 0; u < kKeys / 16; ++u) {
-      const int page = page_of(key0 / 16 + u);
-      src.hidden |= (page < 0) << u;
-      if (u == wave) mine = page;
-    }
-    const int i = key0 / 16 + wave;
-    src.off = max(mine, 0) * d.s_page + (int64_t)kvh * d.s_head + (int64_t)(i % p16) * 16 * d.s_token;
-    src.bytes = mine < 0 ? 0 : max(0, min(16, len - 16 * i)) * 2 * (int)d.s_token;
+    const int i = key0 / 16 + wave, left = len - 16 * i, c = column_of(d, i);
+    const int page = left > 0 ? uniform(scalar_load(row_table, c)) : -1;
+    const bool is = (uint32_t)page < (uint32_t)d.num_pages;
+    src.off = (is ? page : 0) * d.s_page + head_off + (int64_t)((i - c * p16) * 16) * d.s_token;
+    src.bytes = is ? min(16, left) * row_bytes : 0;
+    src.hidden = !is && left > 0;
     return src;
   };
   const uint32_t lds = lds_offset(s_kv), mine_at = 16 * wave * D * 2;
-  const auto load_tile = [&](const uint16_t *base, const Source &src, uint32_t to, const int *from) {
-    const u32x4_t r = buffer_words(base + src.off, src.bytes);
+  const auto load_keys = [&](const Source &src, uint32_t to) {
+    const u32x4_t r = buffer_words(d.k + src.off, src.bytes);
 #pragma unroll
     for (int j = 0; j < LOADS; ++j)
-      load_to_lds(r, (uint32_t)uniform((int)(to + mine_at + j * RPI * D * 2)), from[j]);
+      load_to_lds(r, (uint32_t)uniform((int)(to + mine_at + j * RPI * D * 2)), k_src[D == 128 ? j & 1 : 0],
+                  uniform(j * RPI * row_bytes));
+  };
+  const auto load_values = [&](const Source &src, uint32_t to) {
+    const u32x4_t r = buffer_words(d.v + src.off, src.bytes);
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+      load_to_lds(r, (uint32_t)uniform((int)(to + mine_at + j * RPI * D * 2)), v_src,
+                  uniform(j * RPI * row_bytes));
   };
 
   // operand addresses in a tile: K row `col`, step 0 (step k: ^ 32 k); V row
   // 4 half + l/4 % 4, dim block 0 (block b: ^ 64 b)
-  const int k_at = col * D * 2 + 16 * (half ^ (col & (CH - 1)));
+  const int k_at = col * D * 2 + 16 * (half ^ (col & 7));
   const int v_at = (4 * half + ((lane & 15) >> 2)) * D * 2 +
                    32 * (((lane >> 4) & 1) ^ v_swizzle<D>((lane & 15) >> 2)) + 8 * (lane & 3);
 
-  f32x16_t acc[DB], s[2];
+  f32x16_t acc[DB], s_even[2], s_odd[2];  // output sums; scores of even and odd tiles
 #pragma unroll
   for (int b = 0; b < DB; ++b)
 #pragma unroll
@@ -213,77 +216,78 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   const auto partly = [&](int key0, int first, int last) {
     return key0 + kKeys - 1 > first || (last - key0 >= window && key0 + kKeys > d.sinks);
   };
-  // scores of a tile's keys 32 u .. 32 u + 31
-  const auto scores = [&](const char *kt, int u) {
-    f32x16_t c;
-#pragma unroll
-    for (int v = 0; v < 16; ++v) c[v] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-      c = mfma_32x32x16<DT>(*(const u32x4_t *)(kt + (k_at ^ (32 * k)) + u * 32 * D * 2), q[k], c);
-    return c;
+  // The operand fragments in the order the products take them: K by (step,
+  // 32-key half), V by (16-key group, dim block).
+  const auto k_frag = [&](const char *kt, int i) {
+    return *(const u32x4_t *)(kt + (k_at ^ (32 * (i >> 1))) + (i & 1) * 32 * D * 2);
   };
+  const auto v_frag = [&](const char *vt, int i) {
+    const char *from = vt + (v_at ^ (64 * (i % DB))) + (i / DB) * 16 * D * 2;
+    const uint2 x = bitcast<uint2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)from));
+    const uint2 y = bitcast<uint2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(from + 8 * D * 2)));
+    return u32x4_t{x.x, x.y, y.x, y.y};
+  };
+  const f32x16_t zeros = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 
   // The tiles that some row of this wave sees are the first w_tiles (those
   // that a window hides from all of its rows are computed and masked).
   const int w_tiles = !active || w_max < 0 ? 0 : min(tiles, tiles - (p_max / kKeys - w_max / kKeys));
   if (tiles > 0) {
     Source now = source_of(key_of(0)), next = now;
-    load_tile(d.k, now, lds, k_src);
+    load_keys(now, lds);
     __builtin_amdgcn_s_waitcnt(0x0F70);
     lds_barrier();
-    load_tile(d.v, now, lds + 2 * TILE, v_src);
+    load_values(now, lds + 2 * TILE);
     if (tiles > 1) {
       next = source_of(key_of(1));
-      load_tile(d.k, next, lds + TILE, k_src);
+      load_keys(next, lds + TILE);
     }
     if (w_tiles > 0) {
-      s[0] = scores(s_kv[0], 0);
-      s[1] = scores(s_kv[0], 1);
+#pragma unroll
+      for (int i = 0; i < 2 * KS; ++i)
+        s_even[i & 1] = mfma_32x32x16<DT>(k_frag(s_kv[0], i), q[i >> 1], i < 2 ? zeros : s_even[i & 1]);
     }
-    for (int t = 0; t < tiles; ++t) {
-      // here: s holds tile t's scores; V of t and K of t + 1 are on their way
-      const int buf = t & 1, key0 = key_of(t), hidden = now.hidden;
+    // Tile t, whose scores s holds; V of t and K of t + 1 are on their way.
+    // Leaves the scores of t + 1 in ahead.  (The loop takes two tiles at a time, so
+    // that the two sets of scores and buffers are fixed registers and addresses.)
+    const auto tile = [&](const int t, const int buf, f32x16_t (&s)[2], f32x16_t (&ahead)[2]) {
+      const int key0 = key_of(t);
       const char *kt = s_kv[buf ^ 1], *vt = s_kv[2 + buf];
       const bool masked = partly(key0, p_min, p_max);
       __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's parts are in LDS
+      int flags = now.hidden ? 1 : 0;
       if (masked) {  // (only V: a score that is no number is replaced, a weight of 0 is not)
-        bool any = false;
+        uint32_t bad = 0;
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
-          u32x4_t *at = (u32x4_t *)(s_kv[2 + buf] + mine_at + j * RPI * D * 2 + 16 * lane);
-          u32x4_t x = *at;
-          uint32_t bad = 0;
+          const u32x4_t x = *(const u32x4_t *)(vt + mine_at + j * RPI * D * 2 + 16 * lane);
 #pragma unroll
           for (int e = 0; e < 4; ++e) bad |= not_finite<DT>(x[e]);
-          if (__any(bad != 0)) {  // left out of the products, added below
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] &= ~((not_finite<DT>(x[e]) >> 15) * 0xFFFFu);
-            *at = x;
-            any = true;
-          }
         }
-        if (lane == 0) s_dirty[buf][wave] = any;
+        flags |= __any(bad != 0) ? 2 : 0;
       }
+      if (lane == 0) s_flags[buf][wave] = flags;
       lds_barrier();
       now = next;
-      if (t + 1 < tiles) load_tile(d.v, now, lds + (2 + (buf ^ 1)) * TILE, v_src);
+      if (t + 1 < tiles) load_values(now, lds + (2 + (buf ^ 1)) * TILE);
       if (t + 2 < tiles) {
         next = source_of(key_of(t + 2));
-        load_tile(d.k, next, lds + buf * TILE, k_src);
+        load_keys(next, lds + buf * TILE);
       }
-      const bool dirty = masked && (s_dirty[buf][0] | s_dirty[buf][1] | s_dirty[buf][2] | s_dirty[buf][3]);
+      const u32x4_t group = *(const u32x4_t *)s_flags[buf];
+      const int any = uniform((int)(group[0] | group[1] | group[2] | group[3]));
+      const bool dirty = any & 2;
       const bool mine = t < w_tiles;
-      if (!mine && !dirty) continue;
+      if (!mine && !dirty) return;
 
-      if (hidden || partly(key0, w_min, w_max) || !is_row) {
+      if ((any & 1) || partly(key0, w_min, w_max)) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
             const int j = key0 + 32 * u + 8 * (v >> 2) + 4 * half + (v & 3);
             const bool sees = (j <= pos) & ((pos - j < window) | (j < d.sinks)) &
-                              (((hidden >> (2 * u + (v >> 3))) & 1) == 0);
+                              ((group[2 * u + (v >> 3)] & 1) == 0);
             s[u][v] = sees ? s[u][v] : -INFINITY;
           }
       }
@@ -302,67 +306,96 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
 #pragma unroll
           for (int v = 0; v < 16; ++v) acc[b][v] *= f;
       }
-      // the weights of 16 keys each, as the column operand of O; meanwhile the
-      // matrix unit forms the next tile's scores
-      u32x4_t p[4];
       const float shift = -m * scale;
-      f32x16_t ahead[2];
+      if (dirty) {
+        // Values that are not finite: how many of a sign (of both, for no
+        // number) a row sees of each dim, as products of ones; then they leave
+        // the tile.
+        constexpr uint32_t kOnes = DT == DT_F16 ? 0x3C003C00u : 0x3F803F80u;
+#pragma unroll 1
+        for (int sign = 0; sign < 2; ++sign) {
+          const uint32_t flip = sign ? 0x80008000u : 0u;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        ahead[u] = scores(kt, u);
+          for (int b = 0; b < DB; ++b) {
+            f32x16_t c = zeros;
 #pragma unroll
-        for (int v = 0; v < 16; v += 2) {
-          const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][v], scale, shift));
-          const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][v + 1], scale, shift));
-          l += a + b;
-          p[2 * u + (v >> 3)][(v >> 1) & 3] = pack_pair<DT>(a, b);
-        }
-      }
-      s[0] = ahead[0];
-      s[1] = ahead[1];
+            for (int g = 0; g < 4; ++g) {
+              u32x4_t x = v_frag(vt, g * DB + b), w;
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int b = 0; b < DB; ++b) {
-          const char *from = vt + (v_at ^ (64 * b)) + g * 16 * D * 2;
-          const uint2 x = bitcast<uint2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)from));
-          const uint2 y = bitcast<uint2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(from + 8 * D * 2)));
-          acc[b] = mfma_32x32x16<DT>(u32x4_t{x.x, x.y, y.x, y.y}, p[g], acc[b]);
-        }
-      if (!dirty) continue;
-      // Values that are not finite, key by key, for the rows that see them.
-      // The weights go through LDS (D = 128: where the K tile was, once every
-      // wave is past it), the values come from memory again.
-      lds_barrier();
-      uint32_t *w_at = (D == 64 ? s_weights : (uint32_t *)kt) + wave * 16 * 64;
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w_at[(4 * g + e) * 64 + lane] = p[g][e];
-      lds_barrier();
-      if (!mine) continue;
-      for (int j = 0; j < kKeys; ++j) {
-        const int key = key0 + j, page = page_of(key / 16);
-        if (page < 0 || key >= len) continue;
-        const int in16 = j & 15, e = (in16 & 3) + 4 * (in16 >> 3);
-        const uint32_t pair = w_at[(4 * (j >> 4) + (e >> 1)) * 64 + col + 32 * ((in16 >> 2) & 1)];
-        const float w = to_f32<DT>((uint16_t)(e & 1 ? pair >> 16 : pair));
-        const bool sees = (key <= pos) & ((pos - key < window) | (key < d.sinks));
-        const uint16_t *from = d.v + page * d.s_page + (int64_t)kvh * d.s_head +
-                               (int64_t)(key % d.page_size) * d.s_token + 4 * half;
-#pragma unroll
-        for (int b = 0; b < DB; ++b)
-#pragma unroll
-          for (int v4 = 0; v4 < 4; ++v4) {  // dims 32 b + 8 v4 + 4 half + 0..3
-            const uint2 x = *(const uint2 *)(from + 32 * b + 8 * v4);
-#pragma unroll
-            for (int e2 = 0; e2 < 4; ++e2) {
-              const uint32_t y = e2 < 2 ? x.x : x.y;
-              const uint16_t bits = (uint16_t)(e2 & 1 ? y >> 16 : y);
-              if (sees & (not_finite<DT>(bits) != 0)) acc[b][4 * v4 + e2] += w * to_f32<DT>(bits);
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t bad = not_finite<DT>(x[e]) >> 15;  // 1 in each half that is not finite
+                // exponent bits only: an infinity, of one sign; else no number
+                const uint32_t frac = x[e] & ~(kExp<DT> | 0x80008000u);
+                const uint32_t nan = (((frac & 0xFFFFu) != 0) | ((uint32_t)((frac >> 16) != 0) << 16)) & bad;
+                const uint32_t take = nan | (bad & ~((x[e] ^ flip) >> 15));
+                x[e] = kOnes & ((take & 0x00010001u) * 0xFFFFu);
+                const float s0 = s[g >> 1][8 * (g & 1) + 2 * e], s1 = s[g >> 1][8 * (g & 1) + 2 * e + 1];
+                w[e] = kOnes & ((s0 != -INFINITY ? 0xFFFFu : 0u) | (s1 != -INFINITY ? 0xFFFF0000u : 0u));
+              }
+              c = mfma_32x32x16<DT>(x, w, c);
             }
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[b][v] += c[v] > 0.f ? (sign ? -INFINITY : INFINITY) : 0.f;
           }
+        }
+        lds_barrier();
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+          u32x4_t *at = (u32x4_t *)(s_kv[2 + buf] + mine_at + j * RPI * D * 2 + 16 * lane);
+          u32x4_t x = *at;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] &= ~((not_finite<DT>(x[e]) >> 15) * 0xFFFFu);
+          *at = x;
+        }
+        lds_barrier();
+        if (!mine) return;
       }
+      // The two products in steps of one MFMA, the next fragments' reads and a
+      // share of the weights' arithmetic, which keeps both units busy; the
+      // compiler's own order bunches each kind.  The next tile's scores go
+      // along with the weights of the first 32 keys, and O's first half of
+      // the keys with those of the last 32.
+      constexpr int NQ = 2 * KS, NP = 4 * DB, AHEAD = 4;
+      u32x4_t p[4], kf[AHEAD], vf[AHEAD];  // p: weights of 16 keys each, the column operand of O
+      float sum[2] = {0.f, 0.f};
+      const auto weights = [&](int e) {  // of scores e and e + 1
+        const int u = e >> 4, v = e & 15;
+        const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][v], scale, shift));
+        const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][v + 1], scale, shift));
+        sum[0] += a;
+        sum[1] += b;
+        p[2 * u + (v >> 3)][(v >> 1) & 3] = pack_pair<DT>(a, b);
+      };
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) kf[i] = k_frag(kt, i);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        ahead[i & 1] = mfma_32x32x16<DT>(kf[i % AHEAD], q[i >> 1], i < 2 ? zeros : ahead[i & 1]);
+        if (i + AHEAD < NQ)
+          kf[i % AHEAD] = k_frag(kt, i + AHEAD);
+        else
+          vf[i + AHEAD - NQ] = v_frag(vt, i + AHEAD - NQ);
+        if (NQ == 8)
+          weights(2 * i);
+        else if (i & 1)
+          weights(i - 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        acc[i % DB] = mfma_32x32x16<DT>(vf[i % AHEAD], p[i / DB], acc[i % DB]);
+        if (i + AHEAD < NP) vf[i % AHEAD] = v_frag(vt, i + AHEAD);
+        if (i < NP / 2) {
+#pragma unroll
+          for (int e = 0; e < 32 / NP; e += 2) weights(16 + 32 / NP * i + e);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      l += sum[0] + sum[1];
+    };
+    for (int t = 0; t < tiles; t += 2) {
+      tile(t, 0, s_even, s_odd);
+      if (t + 1 < tiles) tile(t + 1, 1, s_odd, s_even);
     }
   }
   l = over_halves(l, [](float a, float b) { return a + b; });
