@@ -70,6 +70,12 @@ __device__ __forceinline__ int wave_total(int v) {
   return __builtin_amdgcn_readlane(wave_scan(v), 63);
 }
 
+__device__ __forceinline__ int wave_max(int v) {  // of non-negative values
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v = max(v, __shfl_xor(v, o));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
 // Two fp32 values rounded to nearest even into a packed pair.
 template <int DT>
 __device__ __forceinline__ uint32_t pack_pair(float a, float b) {

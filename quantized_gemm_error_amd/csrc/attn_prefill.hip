@@ -60,47 +60,150 @@ __device__ __forceinline__ int v_swizzle(int t) {
   return D == 128 ? 2 * t + ((t ^ (t >> 1)) & 1) : t;
 }
 
-// Where the rows of work item w (of one key-value head) lie: sequence, its
-// rows and the first of them.  Items are blocks of kRows rows; the last
-// blocks of a batch, which see the most keys, come first.
-struct Block {
-  int b, start, n, row0;  // first token, tokens, first row in the block
+// The 64-key tiles that a block of rows at positions p_min..p_max sees: from
+// position 0 for the sinks, then those from lo_tile on.
+struct Tiles {  // (p_min <= p_max)
+  int sink_tiles, lo_tile, count;
+  __device__ __forceinline__ Tiles(const AttnDesc &d, int p_min, int p_max) {
+    const int lo = d.window > 0 ? max(0, p_min - d.window + 1) : 0;
+    lo_tile = lo / kKeys;
+    sink_tiles = min((min(d.sinks, lo) + kKeys - 1) / kKeys, lo_tile);
+    count = p_max < 0 ? 0 : sink_tiles + p_max / kKeys + 1 - lo_tile;
+  }
 };
-__device__ __forceinline__ bool find_block(const AttnDesc &d, int w, Block &k) {
+
+// A work item of a key-value head: part `part` of `parts` of the tiles of the
+// kRows rows from row0 on of a sequence.
+struct Item {
+  int b, start, n, row0;  // first token, tokens, first row in the block
+  int part, parts;
+  int part_row;           // of the sequence's parts in the workspace, per head
+  int block;              // number of the block in the batch
+};
+
+// Item w of a head, the same computation in every wave.  A sequence's blocks
+// are each cut into as many parts as its longest block has stretches of `per`
+// tiles.  When a call has too few blocks to fill the chip, or some with many
+// tiles, parts of `per` tiles take as long as one part if all run at once, and
+// otherwise the tiles and the starts and joins of the parts spread over the
+// slots, and half a part more at the end; the cheapest of a few sizes is
+// taken, whole blocks among them.
+constexpr int kSlots = 512;      // workgroups that run at once: two to a CU
+constexpr int kMinTiles = 4;     // of a part
+constexpr int kPartTiles = 3;    // what a part's start and its partial sums cost, in tiles
+constexpr int kJoinRows = 100;   // rows of partial sums that are joined in the time of a tile
+constexpr int kMaxParts = 64;
+constexpr int kWhole = 1 << 29;  // tiles per part: no block is cut
+
+__device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_rows, int extra_items,
+                                          Item &k) {
   const int lane = threadIdx.x & 63;
-  const auto span = [&](int b, int &start) {
-    start = b;
-    if (!d.q_starts) return 1;
-    start = max(0, min(d.q_starts[b], d.n_tokens));
-    return max(0, min(d.q_starts[b + 1], d.n_tokens) - start);
+  struct Seq {
+    int start, n, blocks, longest, total;  // tiles of the longest block, of all
   };
-  const auto blocks_of = [&](int b) {
-    int start;
-    return b < d.n_seqs ? (int)(((int64_t)span(b, start) * d.G + kRows - 1) / kRows) : 0;
+  const auto seq_of = [&](int b) {
+    Seq s{b, b < d.n_seqs, 0, 0, 0};
+    if (b >= d.n_seqs) return s;
+    if (d.q_starts) {
+      s.start = max(0, min(d.q_starts[b], d.n_tokens));
+      s.n = max(0, min(d.q_starts[b + 1], d.n_tokens) - s.start);
+    }
+    if (s.n == 0) return s;
+    s.blocks = (s.n * d.G + kRows - 1) / kRows;
+    const int len = cached_len(d, b), first = len - s.n, span = (kRows - 1) / d.G;
+    s.longest = Tiles(d, max(first, len - 1 - span), len - 1).count;
+    s.total = min((s.longest + Tiles(d, first, min(len - 1, first + span)).count + 1) / 2, 1 << 18) *
+              min(s.blocks, 1 << 12);
+    return s;
   };
-  int total = 0;
-  for (int b0 = 0; b0 < d.n_seqs; b0 += 64) total += wave_total(blocks_of(b0 + lane));
-  w = total - 1 - w;
-  if (w < 0) return false;
-  int before = 0;
+  const auto parts_of = [&](const Seq &s, int per) {
+    return per >= kWhole ? 1 : min(kMaxParts, max(1, (int)((uint32_t)(s.longest + per - 1) / (uint32_t)per)));
+  };
+  const Seq mine = seq_of(lane);  // of the first 64 sequences
+  const auto sum = [&](auto value) {
+    int all = wave_total(value(mine));
+    for (int b0 = 64; b0 < d.n_seqs; b0 += 64) all += wave_total(value(seq_of(b0 + lane)));
+    return all;
+  };
+  // (sums that device data of any kind cannot overflow: each term is bounded
+  // by more than a whole cut batch may have)
+  const int blocks = sum([](const Seq &s) { return min(s.blocks, 1 << 18); });
+  const int slots = max(kSlots / d.Hkv, 1);
+  int per = kWhole;
+  if (blocks <= kAttnCounters / d.Hkv && extra_items > 0) {
+    const int total = sum([](const Seq &s) { return s.total; });
+    int most = mine.longest;
+    for (int b0 = 64; b0 < d.n_seqs; b0 += 64) most = max(most, seq_of(b0 + lane).longest);
+    most = wave_max(most);
+    const int even = (total + slots - 1) / slots;
+    // whole blocks
+    int least = blocks <= slots ? most : even + (most + 1) / 2;
+    const int tries = d.n_seqs <= 64 ? 6 : 2;
+    for (int i = 0; i < tries && max(kMinTiles, even) < most; ++i) {
+      // the even share times 1, 1.25, 1.5, 2, 4, 8
+      const int p = max(kMinTiles, (even * (i < 3 ? 4 + i : 1 << i) + 3) / 4);
+      if (p >= most) break;
+      const int items = sum([&](const Seq &s) { return s.blocks * parts_of(s, p); });
+      const int rows = sum([&](const Seq &s) {
+        const int parts = parts_of(s, p);
+        return parts > 1 ? (int)min((int64_t)s.n * d.G * parts, (int64_t)1 << 18) : 0;
+      });
+      // the join of the block with the most partial sums
+      int join = 0;
+      for (int b0 = 0; b0 < d.n_seqs; b0 += 64) {
+        const Seq s = b0 == 0 ? mine : seq_of(b0 + lane);
+        const int parts = s.blocks > 0 ? parts_of(s, p) : 1;
+        join = max(join, parts > 1 ? parts * min(s.n * d.G, kRows) : 0);
+      }
+      join = (wave_max(join) + kJoinRows - 1) / kJoinRows;
+      const int cost = kPartTiles + join + (items <= slots ? p : even + (p + 1) / 2);
+      if (rows <= part_rows && items <= blocks + extra_items && cost < least) {
+        least = cost;
+        per = p;
+      }
+    }
+  }
+  const int items = sum([&](const Seq &s) { return s.blocks * parts_of(s, per); });
+  // The last items, which see the most keys, come first; of up to two rounds,
+  // the second in the opposite order, as its items share the first's CUs.
+  const int first_round = max(kSlots / 2 / d.Hkv, 1);
+  if (w >= items) return false;
+  w = w < first_round || items > 2 * first_round ? items - 1 - w : w - first_round;
+  int before = 0, rows_before = 0, blocks_before = 0;
   for (int b0 = 0; b0 < d.n_seqs; b0 += 64) {
-    const int n = blocks_of(b0 + lane), upto = before + wave_scan(n);
+    const Seq s = b0 == 0 ? mine : seq_of(b0 + lane);
+    const int parts = parts_of(s, per), n = s.blocks * parts;
+    const int upto = before + wave_scan(n);
+    const int rows_upto = rows_before + wave_scan(parts > 1 ? s.n * d.G * parts : 0);
+    const int blocks_upto = blocks_before + wave_scan(s.blocks);
     const int all = __builtin_amdgcn_readlane(upto, 63);
     if (w < all) {
       const int at = __builtin_popcountll(__ballot(upto <= w));
       k.b = b0 + at;
       if (k.b >= d.n_seqs) return false;
-      k.row0 = kRows * (w - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(n, at)));
-      k.n = span(k.b, k.start);
-      return k.row0 >= 0 && k.row0 < (int64_t)k.n * d.G;
+      const auto pick = [&](int v) { return __builtin_amdgcn_readlane(v, at); };
+      k.start = pick(s.start);
+      k.n = pick(s.n);
+      k.parts = pick(parts);
+      const int i = w - (pick(upto) - pick(n));
+      k.part = i % k.parts;
+      k.block = i / k.parts;
+      k.row0 = kRows * k.block;
+      k.block += pick(blocks_upto) - pick(s.blocks);
+      k.part_row = pick(rows_upto) - (k.parts > 1 ? k.n * d.G * k.parts : 0);
+      return k.row0 >= 0 && k.row0 < k.n * d.G;
     }
     before = all;
+    rows_before = __builtin_amdgcn_readlane(rows_upto, 63);
+    blocks_before = __builtin_amdgcn_readlane(blocks_upto, 63);
   }
   return false;
 }
 
 template <int DT, int D>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d, int part_rows, int extra_items,
+                                                                     uint32_t *counters, float *parts,
+                                                                     int part_bytes) {
   constexpr int CH = D / 8;          // 16-byte chunks of a row
   constexpr int KS = D / 16;         // contraction steps of S
   constexpr int DB = D / 32;         // 32-dim blocks of O
@@ -113,9 +216,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int kvh = blockIdx.x % d.Hkv;
-  Block blk;
-  if (!find_block(d, blockIdx.x / d.Hkv, blk)) return;
-  blk = {uniform(blk.b), uniform(blk.start), uniform(blk.n), uniform(blk.row0)};
+  Item blk;
+  if (!find_item(d, blockIdx.x / d.Hkv, part_rows, extra_items, blk)) return;
+  blk = {uniform(blk.b), uniform(blk.start), uniform(blk.n), uniform(blk.row0), uniform(blk.part),
+         uniform(blk.parts), uniform(blk.part_row), uniform(blk.block)};
 
   const int len = uniform(cached_len(d, blk.b)), past = len - blk.n;  // position of the first new token
   const int all_rows = blk.n * d.G;
@@ -130,13 +234,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   const int w_end = min(wrow0 + 32, all_rows);
   const int w_min = past + wrow0 / d.G, w_max = past + (w_end - 1) / d.G;
 
-  // the 64-key tiles that some row sees: from position 0 for the sinks, then
-  // from lo_tile on
-  const int lo = d.window > 0 ? max(0, p_min - d.window + 1) : 0;
-  const int lo_tile = lo / kKeys;
-  const int sink_tiles = min((min(d.sinks, lo) + kKeys - 1) / kKeys, lo_tile);
-  const int tiles = p_max < 0 ? 0 : sink_tiles + p_max / kKeys + 1 - lo_tile;
-  const auto key_of = [&](int t) { return kKeys * (t < sink_tiles ? t : t - sink_tiles + lo_tile); };
+  // the part's tiles, counted from the part's first
+  const Tiles list(d, p_min, p_max);
+  const int first = blk.parts == 1 ? 0 : (int)((int64_t)list.count * blk.part / blk.parts);
+  const int tiles = (blk.parts == 1 ? list.count : (int)((int64_t)list.count * (blk.part + 1) / blk.parts)) - first;
+  const auto key_of = [&](int t) {
+    t += first;
+    return kKeys * (t < list.sink_tiles ? t : t - list.sink_tiles + list.lo_tile);
+  };
 
   // queries, the column operand of S
   u32x4_t q[KS];
@@ -231,7 +336,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
 
   // The tiles that some row of this wave sees are the first w_tiles (those
   // that a window hides from all of its rows are computed and masked).
-  const int w_tiles = !active || w_max < 0 ? 0 : min(tiles, tiles - (p_max / kKeys - w_max / kKeys));
+  const int w_tiles =
+      !active || w_max < 0 ? 0 : min(tiles, list.count - (p_max / kKeys - w_max / kKeys) - first);
   if (tiles > 0) {
     Source now = source_of(key_of(0)), next = now;
     load_keys(now, lds);
@@ -356,6 +462,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
       // along with the weights of the first 32 keys, and O's first half of
       // the keys with those of the last 32.
       constexpr int NQ = 2 * KS, NP = 4 * DB, AHEAD = 4;
+      // (this wave's turn over the other one of its SIMD until the products are
+      // out, so that the two take the matrix unit by turns: 984 -> 932 us for
+      // 2048 rows of 64 heads over 16384 keys)
+      __builtin_amdgcn_s_setprio(1);
       u32x4_t p[4], kf[AHEAD], vf[AHEAD];  // p: weights of 16 keys each, the column operand of O
       float sum[2] = {0.f, 0.f};
       const auto weights = [&](int e) {  // of scores e and e + 1
@@ -391,6 +501,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      __builtin_amdgcn_s_setprio(0);
       l += sum[0] + sum[1];
     };
     for (int t = 0; t < tiles; t += 2) {
@@ -399,29 +510,108 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
     }
   }
   l = over_halves(l, [](float a, float b) { return a + b; });
-  if (!is_row) return;
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  uint16_t *to = d.out + (int64_t)(blk.start + tok) * d.o_tok + head * d.o_head + 4 * half;
+  const auto finish = [&](int r, float total, float lse, f32x4_t o, int c) {  // dims c.. of row r
+    const int t = r / d.G, h = kvh * d.G + r - t * d.G;
+    const float inv = total != 0.f ? 1.f / total : 0.f;
+    *(uint2 *)(d.out + (int64_t)(blk.start + t) * d.o_tok + h * d.o_head + c) =
+        uint2{pack_pair<DT>(o[0] * inv, o[1] * inv), pack_pair<DT>(o[2] * inv, o[3] * inv)};
+    if (d.lse && c == 0)
+      d.lse[(int64_t)(blk.start + t) * d.Hq + h] =
+          total != 0.f ? (lse + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+  };
+  const auto dims = [&](int b, int v) {
+    return f32x4_t{acc[b][v], acc[b][v + 1], acc[b][v + 2], acc[b][v + 3]};
+  };
+  if (blk.parts == 1) {
+    if (!is_row) return;
 #pragma unroll
-  for (int b = 0; b < DB; ++b)
+    for (int b = 0; b < DB; ++b)
 #pragma unroll
-    for (int v = 0; v < 16; v += 4)
-      *(uint2 *)(to + 32 * b + 2 * v) = uint2{pack_pair<DT>(acc[b][v] * inv, acc[b][v + 1] * inv),
-                                              pack_pair<DT>(acc[b][v + 2] * inv, acc[b][v + 3] * inv)};
-  if (d.lse && half == 0)
-    d.lse[(int64_t)(blk.start + tok) * d.Hq + head] =
-        l != 0.f ? (m * scale + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+      for (int v = 0; v < 16; v += 4) finish(row, l, m * scale, dims(b, v), 32 * b + 2 * v + 4 * half);
+    return;
+  }
+
+  // The block's parts meet in the workspace; the workgroup that completes
+  // them joins them in order.
+  const auto rs = __builtin_amdgcn_make_buffer_rsrc(parts, (short)0, part_bytes, 0x00020000);
+  const auto part_at = [&](int part, int r) {  // byte offset of a row's part
+    return (kvh * part_rows + blk.part_row + part * all_rows + r) * (D + 4) * 4;
+  };
+  if (is_row) {
+    const int at = part_at(blk.part, row);
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; v += 4) store_partials4(dims(b, v), rs, at + 4 * (32 * b + 2 * v + 4 * half));
+    if (half == 0) store_partials4(f32x4_t{m, l, 0.f, 0.f}, rs, at + 4 * D);
+  }
+  publish_wait();
+  lds_barrier();
+  uint32_t *counter = counters + blk.block * d.Hkv + kvh;
+  if (threadIdx.x == 0)
+    s_flags[0][0] = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                    (uint32_t)blk.parts - 1;
+  lds_barrier();
+  if (!s_flags[0][0]) return;
+  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const int rows = min(kRows, all_rows - blk.row0);
+  for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * kWaves) {
+    const int r = blk.row0 + i / (D / 4), c = 4 * (i % (D / 4));
+    float M = kNoMax, L = 0.f;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < blk.parts; k0 += 4) {
+      f32x4_t po[4], ml[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int at = part_at(min(k0 + u, blk.parts - 1), r);
+        po[u] = load_partials4(rs, at + 4 * c);
+        ml[u] = load_partials4(rs, at + 4 * D);
+      }
+      float M2 = M;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) M2 = fmaxf(M2, ml[u][0]);
+      const float f = __builtin_amdgcn_exp2f((M - M2) * scale);
+      o *= f;
+      L *= f;
+      M = M2;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (k0 + u >= blk.parts) continue;
+        const float w = __builtin_amdgcn_exp2f((ml[u][0] - M) * scale);
+        o += w * po[u];
+        L += w * ml[u][1];
+      }
+    }
+    finish(r, L, M * scale, o, c);
+  }
+}
+
+// Rows of partial sums per head that a call may need: as many as the parts of
+// two rounds of workgroups hold, or all rows in kMaxParts parts.
+int part_rows_of(int Hq, int Hkv, int n_tokens) {
+  return (int)std::min<int64_t>(std::max(2 * kSlots / Hkv, 1) * kRows,
+                                (int64_t)kMaxParts * n_tokens * (Hq / Hkv));
 }
 
 }  // namespace
 
-size_t attn_prefill_workspace(int D, int Hq, int Hkv, int n_seqs, int n_tokens) { return 0; }
+size_t attn_prefill_workspace(int D, int Hq, int Hkv, int n_seqs, int n_tokens) {
+  return kAttnDataOff + (size_t)part_rows_of(Hq, Hkv, n_tokens) * Hkv * (D + 4) * sizeof(float);
+}
 
 hipError_t launch_attn_prefill(const AttnDesc &d, void *ws, hipStream_t s) {
+  // Every block of whole rows, and the items that cutting some may add: up to
+  // a full round of workgroups, or a round more where sequences may differ in
+  // length; none from four rounds on, whose end is short anyway.
   const int64_t blocks = (int64_t)d.n_tokens * d.G / kRows + d.n_seqs;
+  const int slots = std::max(kSlots / d.Hkv, 1), part_rows = part_rows_of(d.Hq, d.Hkv, d.n_tokens);
+  const int extra = blocks < slots ? slots - (int)blocks : blocks < 4 * slots && d.n_seqs > 1 ? slots : 0;
+  const int64_t items = blocks + extra;
   auto *k = d.D == 64 ? (d.dtype == DT_F16 ? attn_prefill_kernel<DT_F16, 64> : attn_prefill_kernel<DT_BF16, 64>)
                       : (d.dtype == DT_F16 ? attn_prefill_kernel<DT_F16, 128> : attn_prefill_kernel<DT_BF16, 128>);
-  hipLaunchKernelGGL(k, dim3((unsigned)(blocks * d.Hkv)), dim3(64 * kWaves), 0, s, d);
+  hipLaunchKernelGGL(k, dim3((unsigned)(items * d.Hkv)), dim3(64 * kWaves), 0, s, d, part_rows, extra,
+                     (uint32_t *)ws, (float *)((char *)ws + kAttnDataOff),
+                     (int)((size_t)part_rows * d.Hkv * (d.D + 4) * sizeof(float)));
   return hipGetLastError();
 }
 
