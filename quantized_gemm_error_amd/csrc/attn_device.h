@@ -71,9 +71,13 @@ __device__ __forceinline__ int wave_total(int v) {
 }
 
 __device__ __forceinline__ int wave_max(int v) {  // of non-negative values
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v = max(v, __shfl_xor(v, o));
-  return __builtin_amdgcn_readfirstlane(v);
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
 // Two fp32 values rounded to nearest even into a packed pair.
@@ -128,18 +132,40 @@ __device__ __forceinline__ u32x4_t buffer_words(const void *p, int bytes) {
                  (uint32_t)uniform(bytes), 0x00020000u};
 }
 
-// 16 bytes per lane from a buffer to LDS: lane i's, at byte_off + at, go to LDS
-// byte lds + 16 i (at and lds are wave-uniform).
-// Bytes past the buffer's range read as zeros.  Written out because the
-// compiler waits for every such load before any later LDS read; the caller
-// waits (vmcnt) before a barrier instead.  It writes no register but m0, which
-// needs one wait state before the load reads it and is used by nothing else
-// in these kernels.
-__device__ __forceinline__ void load_to_lds(u32x4_t buffer, uint32_t lds, int byte_off, int at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :
-               : "s"(lds), "v"(byte_off), "s"(buffer), "s"(at)
-               : "memory");
+// 16 bytes per lane from a buffer to LDS, N times: load j brings lane i's, at
+// byte j step + (j odd ? odd : even), to LDS byte lds + 1024 j + 16 i (lds and
+// step are wave-uniform).  Bytes past the buffer's range read as zeros.
+// Written out because the compiler waits for every such load before any later
+// LDS read; the caller waits (vmcnt) before a barrier instead.  The block
+// writes no register but m0, which nothing else in these kernels uses; the
+// wait states are those of a scalar register that a vector instruction may
+// have written just before (the first load) and of m0.
+template <int N>
+__device__ __forceinline__ void load_to_lds(u32x4_t buffer, uint32_t lds, int even, int odd, int step) {
+  static_assert(N == 2 || N == 4, "loads");
+  if constexpr (N == 2) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 4\n\t"
+        "buffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+        "buffer_load_dwordx4 %2, %3, %4 offen lds"
+        :
+        : "s"(lds), "v"(even), "v"(odd), "s"(buffer), "s"(step)
+        : "memory", "scc");
+  } else {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 4\n\t"
+        "buffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+        "buffer_load_dwordx4 %2, %3, %4 offen lds\n\t"
+        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %3, %5 offen lds\n\t"
+        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+        "buffer_load_dwordx4 %2, %3, %6 offen lds"
+        :
+        : "s"(lds), "v"(even), "v"(odd), "s"(buffer), "s"(step), "s"(2 * step), "s"(3 * step)
+        : "memory", "scc");
+  }
 }
 
 // Read-only words at wave-uniform addresses, through the scalar cache: their

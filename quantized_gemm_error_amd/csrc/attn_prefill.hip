@@ -139,7 +139,7 @@ __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_row
     // whole blocks
     int least = blocks <= slots ? most : even + (most + 1) / 2;
     const int tries = d.n_seqs <= 64 ? 6 : 2;
-    for (int i = 0; i < tries && max(kMinTiles, even) < most; ++i) {
+    for (int i = 0; i < tries && most > 3 * kMinTiles; ++i) {
       // the even share times 1, 1.25, 1.5, 2, 4, 8
       const int p = max(kMinTiles, (even * (i < 3 ? 4 + i : 1 << i) + 3) / 4);
       if (p >= most) break;
@@ -164,9 +164,10 @@ __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_row
     }
   }
   const int items = sum([&](const Seq &s) { return s.blocks * parts_of(s, per); });
-  // The last items, which see the most keys, come first; of up to two rounds,
-  // the second in the opposite order, as its items share the first's CUs.
-  const int first_round = max(kSlots / 2 / d.Hkv, 1);
+  // The last items, which see the most keys, come first; of up to two
+  // workgroups a CU, the second ones, which a launch places after every CU has
+  // one, go the other way, so that CUs get like amounts of work.
+  const int first_round = max(slots / 2, 1);
   if (w >= items) return false;
   w = w < first_round || items > 2 * first_round ? items - 1 - w : w - first_round;
   int before = 0, rows_before = 0, blocks_before = 0;
@@ -269,39 +270,40 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
     k_src[j] = lane_row * row_bytes + 16 * (lane_ch ^ ((j * RPI + lane_row) & 7));
   const int v_src = lane_row * row_bytes +
                     16 * ((((lane_ch >> 1) ^ v_swizzle<D>(lane_row)) << 1) | (lane_ch & 1));
-  // Where this wave's 16 keys of the tile at key0 lie; bytes 0: nowhere.
+  // Where this wave's 16 keys of a tile lie, worked out for 64 tiles at a time,
+  // one per lane, so that the loop has no table entry to wait for.
+  const int p16 = d.page_size / 16;
+  const int32_t *row_table = d.table + (int64_t)blk.b * d.width;
+  int64_t src_off = 0;  // elements, of tile (sources' first) + lane
+  int src_bytes = 0;    // 0: past the cached length; kHidden: on no page
+  constexpr int kHidden = -1;
+  const auto sources_from = [&](int t0) {
+    const int i = key_of(t0 + lane) / 16 + wave, left = len - 16 * i, c = column_of(d, i);
+    const bool want = t0 + lane < tiles && left > 0;
+    const int page = want ? row_table[c] : -1;
+    const bool is = (uint32_t)page < (uint32_t)d.num_pages;
+    src_off = (is ? page : 0) * d.s_page + (int64_t)kvh * d.s_head + (int64_t)((i - c * p16) * 16) * d.s_token;
+    src_bytes = is ? min(16, left) * row_bytes : want ? kHidden : 0;
+  };
   struct Source {
     int64_t off;
     int bytes;
-    bool hidden;  // in the cached length, but on no page
   };
-  const int p16 = d.page_size / 16;
-  const int32_t *row_table = d.table + (int64_t)blk.b * d.width;
-  const int64_t head_off = (int64_t)kvh * d.s_head;
-  const auto source_of = [&](int key0) {
-    Source src;
-    const int i = key0 / 16 + wave, left = len - 16 * i, c = column_of(d, i);
-    const int page = left > 0 ? uniform(scalar_load(row_table, c)) : -1;
-    const bool is = (uint32_t)page < (uint32_t)d.num_pages;
-    src.off = (is ? page : 0) * d.s_page + head_off + (int64_t)((i - c * p16) * 16) * d.s_token;
-    src.bytes = is ? min(16, left) * row_bytes : 0;
-    src.hidden = !is && left > 0;
-    return src;
+  const auto source_of = [&](int t) {
+    if ((t & 63) == 0) sources_from(t);
+    return Source{((int64_t)__builtin_amdgcn_readlane((int)(src_off >> 32), t & 63) << 32) |
+                      (uint32_t)__builtin_amdgcn_readlane((int)src_off, t & 63),
+                  __builtin_amdgcn_readlane(src_bytes, t & 63)};
   };
   const uint32_t lds = lds_offset(s_kv), mine_at = 16 * wave * D * 2;
+  static_assert(RPI * D * 2 == 1024, "a load's rows follow the last load's in LDS");
   const auto load_keys = [&](const Source &src, uint32_t to) {
-    const u32x4_t r = buffer_words(d.k + src.off, src.bytes);
-#pragma unroll
-    for (int j = 0; j < LOADS; ++j)
-      load_to_lds(r, (uint32_t)uniform((int)(to + mine_at + j * RPI * D * 2)), k_src[D == 128 ? j & 1 : 0],
-                  uniform(j * RPI * row_bytes));
+    load_to_lds<LOADS>(buffer_words(d.k + src.off, max(src.bytes, 0)), (uint32_t)uniform((int)(to + mine_at)),
+                       k_src[0], k_src[D == 128 ? 1 : 0], uniform(RPI * row_bytes));
   };
   const auto load_values = [&](const Source &src, uint32_t to) {
-    const u32x4_t r = buffer_words(d.v + src.off, src.bytes);
-#pragma unroll
-    for (int j = 0; j < LOADS; ++j)
-      load_to_lds(r, (uint32_t)uniform((int)(to + mine_at + j * RPI * D * 2)), v_src,
-                  uniform(j * RPI * row_bytes));
+    load_to_lds<LOADS>(buffer_words(d.v + src.off, max(src.bytes, 0)), (uint32_t)uniform((int)(to + mine_at)),
+                       v_src, v_src, uniform(RPI * row_bytes));
   };
 
   // operand addresses in a tile: K row `col`, step 0 (step k: ^ 32 k); V row
@@ -332,6 +334,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
     const uint2 y = bitcast<uint2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(from + 8 * D * 2)));
     return u32x4_t{x.x, x.y, y.x, y.y};
   };
+  constexpr int NQ = 2 * KS, NP = 4 * DB, AHEAD = 4;  // steps of the products, fragments read ahead
   const f32x16_t zeros = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 
   // The tiles that some row of this wave sees are the first w_tiles (those
@@ -339,13 +342,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   const int w_tiles =
       !active || w_max < 0 ? 0 : min(tiles, list.count - (p_max / kKeys - w_max / kKeys) - first);
   if (tiles > 0) {
-    Source now = source_of(key_of(0)), next = now;
+    Source now = source_of(0), next = now;
     load_keys(now, lds);
     __builtin_amdgcn_s_waitcnt(0x0F70);
     lds_barrier();
     load_values(now, lds + 2 * TILE);
     if (tiles > 1) {
-      next = source_of(key_of(1));
+      next = source_of(1);
       load_keys(next, lds + TILE);
     }
     if (w_tiles > 0) {
@@ -361,7 +364,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
       const char *kt = s_kv[buf ^ 1], *vt = s_kv[2 + buf];
       const bool masked = partly(key0, p_min, p_max);
       __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's parts are in LDS
-      int flags = now.hidden ? 1 : 0;
+      int flags = now.bytes == kHidden ? 1 : 0;
       if (masked) {  // (only V: a score that is no number is replaced, a weight of 0 is not)
         uint32_t bad = 0;
 #pragma unroll
@@ -374,13 +377,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
       }
       if (lane == 0) s_flags[buf][wave] = flags;
       lds_barrier();
+      // (first the reads whose latency the loads' issue covers)
+      const u32x4_t group = *(const u32x4_t *)s_flags[buf];
+      u32x4_t kf[AHEAD], vf[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) kf[i] = k_frag(kt, i);
       now = next;
       if (t + 1 < tiles) load_values(now, lds + (2 + (buf ^ 1)) * TILE);
       if (t + 2 < tiles) {
-        next = source_of(key_of(t + 2));
+        next = source_of(t + 2);
         load_keys(next, lds + buf * TILE);
       }
-      const u32x4_t group = *(const u32x4_t *)s_flags[buf];
       const int any = uniform((int)(group[0] | group[1] | group[2] | group[3]));
       const bool dirty = any & 2;
       const bool mine = t < w_tiles;
@@ -461,12 +468,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
       // compiler's own order bunches each kind.  The next tile's scores go
       // along with the weights of the first 32 keys, and O's first half of
       // the keys with those of the last 32.
-      constexpr int NQ = 2 * KS, NP = 4 * DB, AHEAD = 4;
       // (this wave's turn over the other one of its SIMD until the products are
       // out, so that the two take the matrix unit by turns: 984 -> 932 us for
       // 2048 rows of 64 heads over 16384 keys)
       __builtin_amdgcn_s_setprio(1);
-      u32x4_t p[4], kf[AHEAD], vf[AHEAD];  // p: weights of 16 keys each, the column operand of O
+      u32x4_t p[4];  // p: weights of 16 keys each, the column operand of O
       float sum[2] = {0.f, 0.f};
       const auto weights = [&](int e) {  // of scores e and e + 1
         const int u = e >> 4, v = e & 15;
@@ -476,8 +482,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
         sum[1] += b;
         p[2 * u + (v >> 3)][(v >> 1) & 3] = pack_pair<DT>(a, b);
       };
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) kf[i] = k_frag(kt, i);
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
         ahead[i & 1] = mfma_32x32x16<DT>(kf[i % AHEAD], q[i >> 1], i < 2 ? zeros : ahead[i & 1]);
