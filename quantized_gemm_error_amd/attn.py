@@ -82,17 +82,24 @@ def load_library():
     return lib
 
 
+def _lib():
+    return _bound if _bound is not None else load_library()
+
+
 def _int32(t, name: str, dim: int, device=None) -> None:
     import torch
+    if (t is not None and t.dtype is torch.int32 and t.dim() == dim and t.is_contiguous()
+            and (device is None or t.device == device)):
+        return
     _require(t is not None, f"{name} is missing")
     _require(t.dtype == torch.int32, f"{name} has dtype {t.dtype}, expected torch.int32", TypeError)
     _require(t.dim() == dim and t.is_contiguous(), f"{name} must be a contiguous {dim}-D tensor")
-    if device is not None:
-        _require(t.device == device, f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _gpu(device) -> None:
-    _require(device.type == "cuda", f"tensors must be on a GPU, got {device}")
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
 
 
 class _On:
@@ -102,9 +109,12 @@ class _On:
         import torch
         self.given = stream is not None
         if stream is None:
-            stream = torch.cuda.current_stream(device)
-        self.stream = stream
-        self.ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+            # (the handle alone where torch offers it: a Stream object costs 2 us)
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            self.ptr = raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
+        else:
+            self.stream = stream
+            self.ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
         self.guard = None if torch.cuda.current_device() == device.index else \
             torch.cuda.device(device)
 
@@ -118,17 +128,16 @@ class _On:
             self.guard.__exit__(*exc)
 
     def made(self, *tensors):
-        """Tensors allocated by the call (on the current stream) and written on a given one."""
-        if self.given:
-            import torch
-            st = self.stream
-            if not hasattr(st, "cuda_stream"):
-                st = torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()
-            here = torch.cuda.current_stream(tensors[0].device)
-            if st.cuda_stream != here.cuda_stream:
-                st.wait_stream(here)  # what the memory served before ends first
-                for t in tensors:
-                    t.record_stream(st)
+        """Tensors allocated by the call (on the current stream) and written on the given one."""
+        import torch
+        st = self.stream
+        if not hasattr(st, "cuda_stream"):
+            st = torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()
+        here = torch.cuda.current_stream(tensors[0].device)
+        if st.cuda_stream != here.cuda_stream:
+            st.wait_stream(here)  # what the memory served before ends first
+            for t in tensors:
+                t.record_stream(st)
 
 
 class SpearKVCache:
@@ -151,6 +160,8 @@ class SpearKVCache:
         _require(max(shape) < 2 ** 31, f"cache of shape {tuple(k.shape)} is too large")
         self.k, self.v, self.device = k, v, k.device
         self.n_layers, self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = shape
+        self.dtype, self.scale = k.dtype, 1.0 / math.sqrt(self.head_dim)
+        self.spans = _span(k), _span(v)
         self.c = SpearKVCacheC(k.data_ptr(), v.data_ptr(), code, *shape, *strides[:4])
         self.ref = ctypes.byref(self.c)
 
@@ -178,14 +189,15 @@ class SpearKVBatch:
         self.n_seqs = n
         self.c = SpearKVBatchC(n, width, n, block_table.data_ptr(), kv_lens.data_ptr(),
                                None if q_starts is None else q_starts.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
     def rows(self, n_tokens: int):
-        """The C struct for a call with this many rows."""
-        if n_tokens == self.c.n_tokens:
-            return ctypes.byref(self.c)
-        c = SpearKVBatchC.from_buffer_copy(self.c)
-        c.n_tokens = n_tokens
-        return ctypes.byref(c)
+        """The C struct for a call with this many rows (kept: a step's calls have as many)."""
+        if n_tokens != self.c.n_tokens:
+            c = SpearKVBatchC.from_buffer_copy(self.c)
+            c.n_tokens = n_tokens
+            self.c, self.ref = c, ctypes.byref(c)
+        return self.ref
 
 
 class SpearKVPool:
@@ -235,67 +247,78 @@ def new_attn_workspace(cache: SpearKVCache, n_q_heads: int, n_seqs: int, n_token
     return buf[off:off + n]
 
 
-def _rows(t, name: str, cache, tokens=None, heads=None) -> None:
-    """t is [tokens][heads][head_dim] of the cache's dtype, its last dimension contiguous."""
+def _rows(t, name: str, cache, tokens=None, heads=None):
+    """t is [tokens][heads][head_dim] of the cache's dtype, its last dimension contiguous -> its
+    sizes and strides.  (One test for all on the call path; the message is found afterwards.)"""
+    if t.dim() == 3:
+        (T, H, D), (st, sh, sd) = t.shape, t.stride()
+        if (D == cache.head_dim and sd == 1 and t.dtype is cache.dtype and t.device == cache.device
+                and (tokens is None or T == tokens) and (heads is None or H == heads)):
+            return T, H, st, sh
     _require(t.dim() == 3, f"{name} must be [tokens][heads][head_dim], got {t.dim()}-D")
-    _require(t.dtype == cache.k.dtype, f"{name} has dtype {t.dtype}, the cache {cache.k.dtype}", TypeError)
-    shape = t.shape
-    _require(shape[2] == cache.head_dim and (tokens is None or shape[0] == tokens)
-             and (heads is None or shape[1] == heads),
-             f"{name} has shape {tuple(shape)}, expected "
+    _require(t.dtype == cache.dtype, f"{name} has dtype {t.dtype}, the cache {cache.dtype}", TypeError)
+    _require(t.shape[2] == cache.head_dim and (tokens is None or t.shape[0] == tokens)
+             and (heads is None or t.shape[1] == heads),
+             f"{name} has shape {tuple(t.shape)}, expected "
              f"({'any' if tokens is None else tokens}, {'any' if heads is None else heads}, {cache.head_dim})")
     _require(t.stride(2) == 1, f"the last dimension of {name} must be contiguous")
-    _require(t.device == cache.device, f"{name} is on {t.device}, the cache on {cache.device}")
+    raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
 
 
-def _overlap(a, b) -> bool:
-    """Whether the address ranges of two tensors meet."""
-    def span(t):
-        return t.data_ptr(), t.data_ptr() + t.element_size() * (
-            1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
-    if a.numel() == 0 or b.numel() == 0:
-        return False
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
+def _span(t):
+    """The addresses of a tensor's first byte and past its last one."""
+    at = t.data_ptr()
+    if t.numel() == 0:
+        return at, at
+    return at, at + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+
+
+def _meet(a, b) -> bool:
+    return a[0] < b[1] and b[0] < a[1]
 
 
 def _attention(fn, cache, batch, q, out, scale, window, sinks, workspace, return_lse, stream, decode):
     import torch
-    _rows(q, "q", cache)
-    T, Hq, D = q.shape
-    _require(batch.device == cache.device, f"the batch is on {batch.device}, the cache on {cache.device}")
+    T, Hq, q_tok, q_head = _rows(q, "q", cache)
+    device = cache.device
+    if batch.device != device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {device}")
     if batch.q_starts is None:
-        _require(T == batch.n_seqs, f"q has {T} rows for {batch.n_seqs} sequences of one token")
-    else:
-        _require(not decode, "decode takes one token per sequence: the batch has q_starts")
+        if T != batch.n_seqs:
+            raise ValueError(f"q has {T} rows for {batch.n_seqs} sequences of one token")
+    elif decode:
+        raise ValueError("decode takes one token per sequence: the batch has q_starts")
     if out is not None:
-        _rows(out, "out", cache, T, Hq)
-        _require(not _overlap(out, q), "out must not overlap q")
-        _require(not _overlap(out, cache.k) and not _overlap(out, cache.v),
+        _, _, o_tok, o_head = _rows(out, "out", cache, T, Hq)
+        span = _span(out)
+        _require(not _meet(span, _span(q)), "out must not overlap q")
+        _require(not _meet(span, cache.spans[0]) and not _meet(span, cache.spans[1]),
                  "out must not overlap the cache")
+    ws, ws_bytes = None, 0
     if workspace is not None:
-        _require(workspace.is_contiguous() and workspace.device == cache.device,
-                 f"workspace must be contiguous and on {cache.device}")
-    _gpu(cache.device)
-    on = _On(cache.device, stream)
+        if not workspace.is_contiguous() or workspace.device != device:
+            raise ValueError(f"workspace must be contiguous and on {device}")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _gpu(device)
+    on = _On(device, stream)
     made = []
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=cache.device)
+        out = torch.empty((T, Hq, cache.head_dim), dtype=cache.dtype, device=device)
+        o_tok, o_head = Hq * cache.head_dim, cache.head_dim
         made.append(out)
     lse = None
     if return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=cache.device)
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
         made.append(lse)
-    if made:
+    if on.given and made:
         on.made(*made)
-    args = SpearAttnArgsC(Hq, window, sinks, 1.0 / math.sqrt(D) if scale is None else scale,
-                          q.data_ptr(), q.stride(0), q.stride(1),
-                          out.data_ptr(), out.stride(0), out.stride(1),
+    args = SpearAttnArgsC(Hq, window, sinks, cache.scale if scale is None else scale,
+                          q.data_ptr(), q_tok, q_head, out.data_ptr(), o_tok, o_head,
                           None if lse is None else lse.data_ptr())
-    ws, ws_bytes = (None, 0) if workspace is None else \
-        (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     with on as ptr:
-        _check(fn(cache.ref, batch.rows(T), ctypes.byref(args), ws, ws_bytes, ptr))
+        status = fn(cache.ref, batch.rows(T), ctypes.byref(args), ws, ws_bytes, ptr)
+    if status:
+        _check(status)
     return (out, lse) if return_lse else out
 
 
@@ -304,7 +327,7 @@ def spear_attn_decode(cache: SpearKVCache, batch: SpearKVBatch, q, out=None, sca
                       stream=None):
     """q [seqs][heads][dim] -> out of the same shape (and lse [seqs][heads] when asked for).
     scale None: 1 / sqrt(dim).  window 0: none."""
-    return _attention(load_library().spear_attn_decode, cache, batch, q, out, scale, window, sinks,
+    return _attention(_lib().spear_attn_decode, cache, batch, q, out, scale, window, sinks,
                       workspace, return_lse, stream, True)
 
 
@@ -312,36 +335,38 @@ def spear_attn_prefill(cache: SpearKVCache, batch: SpearKVBatch, q, out=None, sc
                        window: int = 0, sinks: int = 0, workspace=None, return_lse: bool = False,
                        stream=None):
     """q [tokens][heads][dim], rows as in the batch's q_starts -> out of the same shape."""
-    return _attention(load_library().spear_attn_prefill, cache, batch, q, out, scale, window, sinks,
+    return _attention(_lib().spear_attn_prefill, cache, batch, q, out, scale, window, sinks,
                       workspace, return_lse, stream, False)
 
 
 def spear_kv_append(cache: SpearKVCache, batch: SpearKVBatch, k, v, stream=None) -> None:
     """Store new keys and values [tokens][kv heads][dim] in the batch's pages."""
-    _rows(k, "k", cache, heads=cache.n_kv_heads)
-    T = k.shape[0]
-    _rows(v, "v", cache, T, cache.n_kv_heads)
-    _require(batch.device == cache.device, f"the batch is on {batch.device}, the cache on {cache.device}")
-    _require(batch.q_starts is not None or T == batch.n_seqs,
-             f"k has {T} rows for {batch.n_seqs} sequences of one token")
-    for new in (k, v):
-        for old in (cache.k, cache.v):
-            _require(not _overlap(new, old), "k and v must not overlap the cache")
+    T, _, k_tok, k_head = _rows(k, "k", cache, heads=cache.n_kv_heads)
+    _, _, v_tok, v_head = _rows(v, "v", cache, T, cache.n_kv_heads)
+    if batch.device != cache.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    if batch.q_starts is None and T != batch.n_seqs:
+        raise ValueError(f"k has {T} rows for {batch.n_seqs} sequences of one token")
+    for span in (_span(k), _span(v)):
+        if _meet(span, cache.spans[0]) or _meet(span, cache.spans[1]):
+            raise ValueError("k and v must not overlap the cache")
     _gpu(cache.device)
     with _On(cache.device, stream) as ptr:
-        _check(load_library().spear_kv_append(
-            cache.ref, batch.rows(T), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-            v.stride(0), v.stride(1), ptr))
+        status = _lib().spear_kv_append(cache.ref, batch.rows(T), k.data_ptr(), v.data_ptr(), k_tok, k_head,
+                                        v_tok, v_head, ptr)
+    if status:
+        _check(status)
 
 
 def spear_kv_copy_pages(cache: SpearKVCache, src, dst, stream=None) -> None:
     """Page src[i] to page dst[i] of all layers (int32 device tensors)."""
     _int32(src, "src", 1, cache.device)
     _int32(dst, "dst", 1, cache.device)
-    _require(src.numel() == dst.numel(), f"src has {src.numel()} entries, dst {dst.numel()}")
+    if src.numel() != dst.numel():
+        raise ValueError(f"src has {src.numel()} entries, dst {dst.numel()}")
     _gpu(cache.device)
     with _On(cache.device, stream) as ptr:
-        _check(load_library().spear_kv_copy_pages(cache.ref, src.data_ptr(), dst.data_ptr(),
+        _check(_lib().spear_kv_copy_pages(cache.ref, src.data_ptr(), dst.data_ptr(),
                                                   src.numel(), ptr))
 
 
@@ -349,10 +374,11 @@ def spear_kv_fork(pool: SpearKVPool, src, dst, stream=None) -> None:
     """Slots dst[i] become copies of slots src[i] that share their pages."""
     _int32(src, "src", 1, pool.device)
     _int32(dst, "dst", 1, pool.device)
-    _require(src.numel() == dst.numel(), f"src has {src.numel()} entries, dst {dst.numel()}")
+    if src.numel() != dst.numel():
+        raise ValueError(f"src has {src.numel()} entries, dst {dst.numel()}")
     _gpu(pool.device)
     with _On(pool.device, stream) as ptr:
-        _check(load_library().spear_kv_fork(pool.ref, src.data_ptr(), dst.data_ptr(), src.numel(), ptr))
+        _check(_lib().spear_kv_fork(pool.ref, src.data_ptr(), dst.data_ptr(), src.numel(), ptr))
 
 
 def spear_kv_reserve(pool: SpearKVPool, cache: SpearKVCache, slots, new_lens, missing=None,
@@ -362,8 +388,10 @@ def spear_kv_reserve(pool: SpearKVPool, cache: SpearKVCache, slots, new_lens, mi
     import torch
     _int32(slots, "slots", 1, pool.device)
     _int32(new_lens, "new_lens", 1, pool.device)
-    _require(slots.numel() == new_lens.numel(), f"slots has {slots.numel()} entries, new_lens {new_lens.numel()}")
-    _require(cache.device == pool.device, f"the cache is on {cache.device}, the pool on {pool.device}")
+    if slots.numel() != new_lens.numel():
+        raise ValueError(f"slots has {slots.numel()} entries, new_lens {new_lens.numel()}")
+    if cache.device != pool.device:
+        raise ValueError(f"the cache is on {cache.device}, the pool on {pool.device}")
     if missing is not None:
         _int32(missing, "missing", 1, pool.device)
         _require(missing.numel() == 1, "missing must hold one value")
@@ -371,9 +399,10 @@ def spear_kv_reserve(pool: SpearKVPool, cache: SpearKVCache, slots, new_lens, mi
     on = _On(pool.device, stream)
     if missing is None:
         missing = torch.empty(1, dtype=torch.int32, device=pool.device)
-        on.made(missing)
+        if on.given:
+            on.made(missing)
     with on as ptr:
-        _check(load_library().spear_kv_reserve(pool.ref, cache.ref, slots.data_ptr(),
+        _check(_lib().spear_kv_reserve(pool.ref, cache.ref, slots.data_ptr(),
                                                new_lens.data_ptr(), slots.numel(),
                                                missing.data_ptr(), ptr))
     return missing
@@ -384,13 +413,14 @@ def spear_kv_free(pool: SpearKVPool, slots, stream=None) -> None:
     _int32(slots, "slots", 1, pool.device)
     _gpu(pool.device)
     with _On(pool.device, stream) as ptr:
-        _check(load_library().spear_kv_free(pool.ref, slots.data_ptr(), slots.numel(), ptr))
+        _check(_lib().spear_kv_free(pool.ref, slots.data_ptr(), slots.numel(), ptr))
 
 
 def spear_kv_compact(pool: SpearKVPool, cache: SpearKVCache, used=None, stream=None):
     """Move the used pages to the lowest indices -> used, an int32 device tensor [1]: how many."""
     import torch
-    _require(cache.device == pool.device, f"the cache is on {cache.device}, the pool on {pool.device}")
+    if cache.device != pool.device:
+        raise ValueError(f"the cache is on {cache.device}, the pool on {pool.device}")
     if used is not None:
         _int32(used, "used", 1, pool.device)
         _require(used.numel() == 1, "used must hold one value")
@@ -398,7 +428,8 @@ def spear_kv_compact(pool: SpearKVPool, cache: SpearKVCache, used=None, stream=N
     on = _On(pool.device, stream)
     if used is None:
         used = torch.empty(1, dtype=torch.int32, device=pool.device)
-        on.made(used)
+        if on.given:
+            on.made(used)
     with on as ptr:
-        _check(load_library().spear_kv_compact(pool.ref, cache.ref, used.data_ptr(), ptr))
+        _check(_lib().spear_kv_compact(pool.ref, cache.ref, used.data_ptr(), ptr))
     return used

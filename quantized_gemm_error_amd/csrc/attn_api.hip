@@ -300,7 +300,7 @@ spear_status_t spear_kv_copy_pages(const spear_kv_cache_t *cache, const int32_t 
   TRY(check_list("src", src, n, kMaxList));
   TRY(check_list("dst", dst, n, kMaxList));
   if (n == 0) return ok();
-  return hip_status(launch_kv_copy_pages(page_desc(*cache), src, dst, n, nullptr, (hipStream_t)stream),
+  return hip_status(launch_kv_copy_pages(page_desc(*cache), src, dst, n, (hipStream_t)stream),
                     "page copy launch");
 }
 

@@ -53,9 +53,8 @@ struct PageDesc {
   int layers, num_pages, H, S, D;
   int64_t s_layer, s_page, s_head, s_token;
 };
-// n pairs; with count != nullptr, only the first *count of them.
 hipError_t launch_kv_copy_pages(const PageDesc &p, const int32_t *src, const int32_t *dst, int n,
-                                const int32_t *count, hipStream_t s);
+                                hipStream_t s);
 hipError_t launch_kv_fork(const spear_kv_pool_t &pool, const int32_t *src, const int32_t *dst,
                           int n, hipStream_t s);
 hipError_t launch_kv_free(const spear_kv_pool_t &pool, const int32_t *slots, int n, hipStream_t s);

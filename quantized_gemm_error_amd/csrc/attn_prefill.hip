@@ -92,7 +92,7 @@ constexpr int kSlots = 512;      // workgroups that run at once: two to a CU
 constexpr int kMinTiles = 4;     // of a part
 constexpr int kPartTiles = 3;    // what a part's start and its partial sums cost, in tiles
 constexpr int kJoinRows = 100;   // rows of partial sums that are joined in the time of a tile
-constexpr int kMaxParts = 64;
+constexpr int kMaxParts = 63;
 constexpr int kWhole = 1 << 29;  // tiles per part: no block is cut
 
 __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_rows, int extra_items,
@@ -211,6 +211,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   constexpr int RPI = 64 / CH;       // rows a wave's load instruction brings
   constexpr int LOADS = 16 / RPI;    // instructions for 16 keys
   constexpr int TILE = kKeys * D * 2;  // bytes of a staged K or V tile
+  static_assert((kMaxParts + 1) * kRows * 4 <= 4 * TILE, "the join's weights");
   __shared__ __attribute__((aligned(256))) char s_kv[4][TILE];  // K tiles of even and odd t, then V's
   __shared__ __attribute__((aligned(16))) int s_flags[2][kWaves];  // of a tile's 16-key groups: 1 hidden, 2 not finite
 
@@ -468,10 +469,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
       // compiler's own order bunches each kind.  The next tile's scores go
       // along with the weights of the first 32 keys, and O's first half of
       // the keys with those of the last 32.
-      // (this wave's turn over the other one of its SIMD until the products are
-      // out, so that the two take the matrix unit by turns: 984 -> 932 us for
-      // 2048 rows of 64 heads over 16384 keys)
-      __builtin_amdgcn_s_setprio(1);
       u32x4_t p[4];  // p: weights of 16 keys each, the column operand of O
       float sum[2] = {0.f, 0.f};
       const auto weights = [&](int e) {  // of scores e and e + 1
@@ -495,6 +492,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
           weights(i - 1);
         __builtin_amdgcn_sched_barrier(0);
       }
+      // (the wave goes before the other one of its SIMD while it has mostly
+      // products to issue: 980 -> 955 us for 2048 rows of 64 heads over 16384 keys)
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         acc[i % DB] = mfma_32x32x16<DT>(vf[i % AHEAD], p[i / DB], acc[i % DB]);
@@ -514,24 +514,23 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
     }
   }
   l = over_halves(l, [](float a, float b) { return a + b; });
-  const auto finish = [&](int r, float total, float lse, f32x4_t o, int c) {  // dims c.. of row r
+  const auto store = [&](int r, f32x4_t o, int c, float lse) {  // dims c.. of row r
     const int t = r / d.G, h = kvh * d.G + r - t * d.G;
-    const float inv = total != 0.f ? 1.f / total : 0.f;
     *(uint2 *)(d.out + (int64_t)(blk.start + t) * d.o_tok + h * d.o_head + c) =
-        uint2{pack_pair<DT>(o[0] * inv, o[1] * inv), pack_pair<DT>(o[2] * inv, o[3] * inv)};
-    if (d.lse && c == 0)
-      d.lse[(int64_t)(blk.start + t) * d.Hq + h] =
-          total != 0.f ? (lse + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+        uint2{pack_pair<DT>(o[0], o[1]), pack_pair<DT>(o[2], o[3])};
+    if (d.lse && c == 0) d.lse[(int64_t)(blk.start + t) * d.Hq + h] = lse;
   };
   const auto dims = [&](int b, int v) {
     return f32x4_t{acc[b][v], acc[b][v + 1], acc[b][v + 2], acc[b][v + 3]};
   };
   if (blk.parts == 1) {
     if (!is_row) return;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const float lse = l != 0.f ? (m * scale + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 #pragma unroll
     for (int b = 0; b < DB; ++b)
 #pragma unroll
-      for (int v = 0; v < 16; v += 4) finish(row, l, m * scale, dims(b, v), 32 * b + 2 * v + 4 * half);
+      for (int v = 0; v < 16; v += 4) store(row, dims(b, v) * inv, 32 * b + 2 * v + 4 * half, lse);
     return;
   }
 
@@ -558,35 +557,60 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   lds_barrier();
   if (!s_flags[0][0]) return;
   if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // First each row's weights of the parts, w_s = 2^((m_s - M) scale) / L, and
+  // M and L; then the sums, with many loads in flight.  LDS is free by now.
   const int rows = min(kRows, all_rows - blk.row0);
-  for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * kWaves) {
-    const int r = blk.row0 + i / (D / 4), c = 4 * (i % (D / 4));
+  float *w_of = (float *)s_kv[0];             // [kMaxParts][kRows]
+  float *lse_of = w_of + kMaxParts * kRows;   // [kRows]
+  for (int r = threadIdx.x; r < rows; r += 64 * kWaves) {
     float M = kNoMax, L = 0.f;
-    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-    for (int k0 = 0; k0 < blk.parts; k0 += 4) {
-      f32x4_t po[4], ml[4];
+    for (int k0 = 0; k0 < blk.parts; k0 += 8) {
+      f32x4_t ml[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int at = part_at(min(k0 + u, blk.parts - 1), r);
-        po[u] = load_partials4(rs, at + 4 * c);
-        ml[u] = load_partials4(rs, at + 4 * D);
-      }
-      float M2 = M;
+      for (int u = 0; u < 8; ++u)
+        ml[u] = load_partials4(rs, part_at(min(k0 + u, blk.parts - 1), blk.row0 + r) + 4 * D);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) M2 = fmaxf(M2, ml[u][0]);
-      const float f = __builtin_amdgcn_exp2f((M - M2) * scale);
-      o *= f;
-      L *= f;
-      M = M2;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
         if (k0 + u >= blk.parts) continue;
-        const float w = __builtin_amdgcn_exp2f((ml[u][0] - M) * scale);
-        o += w * po[u];
-        L += w * ml[u][1];
+        const float M2 = fmaxf(M, ml[u][0]);
+        L = L * __builtin_amdgcn_exp2f((M - M2) * scale) + ml[u][1] * __builtin_amdgcn_exp2f((ml[u][0] - M2) * scale);
+        M = M2;
+        w_of[(k0 + u) * kRows + r] = ml[u][0];
       }
     }
-    finish(r, L, M * scale, o, c);
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    for (int k = 0; k < blk.parts; ++k)
+      w_of[k * kRows + r] = inv * __builtin_amdgcn_exp2f((w_of[k * kRows + r] - M) * scale);
+    lse_of[r] = L != 0.f ? (M * scale + __builtin_amdgcn_logf(L)) * kLn2 : -INFINITY;
+  }
+  lds_barrier();
+  constexpr int AT_ONCE = 4, Q4 = D / 4;
+  for (int i0 = threadIdx.x; i0 < rows * Q4; i0 += AT_ONCE * 64 * kWaves) {
+    f32x4_t o[AT_ONCE];
+    int r[AT_ONCE], at[AT_ONCE];
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {  // (past the last row: the last row again, not stored)
+      const int i = min(i0 + j * 64 * kWaves, rows * Q4 - 1);
+      r[j] = i / Q4;
+      at[j] = 16 * (i % Q4);
+      o[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int k0 = 0; k0 < blk.parts; k0 += 8) {
+      f32x4_t x[AT_ONCE][8];
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j)
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          x[j][u] = load_partials4(rs, part_at(min(k0 + u, blk.parts - 1), blk.row0 + r[j]) + at[j]);
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j)
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (k0 + u < blk.parts) o[j] += w_of[(k0 + u) * kRows + r[j]] * x[j][u];
+    }
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j)
+      if (i0 + j * 64 * kWaves < rows * Q4) store(blk.row0 + r[j], o[j], at[j] / 4, lse_of[r[j]]);
   }
 }
 

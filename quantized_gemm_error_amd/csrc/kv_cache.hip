@@ -4,6 +4,8 @@
 // All of it is index work and 16-byte copies, bound by memory or, at the
 // sizes of one decode step, by launches: each call is one launch for the
 // bookkeeping and, where pages move, one for the bytes.
+#include <algorithm>
+
 #include "attn_internal.h"
 
 namespace spear {
@@ -51,12 +53,47 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendDesc d) {
 
 // -------------------------------------------------------------- page copies
 
-// Workgroup (x, layer and array, y): pairs x, x + gridDim.x, ... of one array
-// of one layer, 16 bytes per thread.
+// What compaction changes besides the pages' bytes: the table's entries and
+// the counts follow their pages.
+struct Rename {
+  spear_kv_pool_t pool;
+  const int32_t *rank, *used;  // place of a moved page in src and dst; pages in use
+};
+
+__device__ void rename(const Rename &n, const int32_t *src, const int32_t *dst, int moves, int64_t i,
+                       int64_t step) {
+  const spear_kv_pool_t &p = n.pool;
+  const int64_t entries = (int64_t)p.n_slots * p.table_width;
+  const int used = *n.used;
+  for (int64_t e = i; e < entries; e += step) {
+    const int page = p.table[e];
+    if (!in_range(page, p.num_pages) || page < used) continue;
+    // (an entry that names a page nobody counts is left as it is)
+    const int r = n.rank[page];
+    if (in_range(r, moves) && src[r] == page) p.table[e] = dst[r];
+  }
+  for (int64_t r = i; r < moves; r += step) {
+    const int a = src[r], b = dst[r];
+    p.refs[b] = p.refs[a];
+    p.refs[a] = 0;
+  }
+}
+
+// Workgroup (x, layer and array, z): pairs x, x + gridDim.x, ... of one array
+// of one layer, 16 bytes per thread.  RENAME: planes of y past the arrays'
+// rename the table.
+template <bool RENAME>
 __global__ __launch_bounds__(kThreads) void copy_pages_kernel(PageDesc p, const int32_t *src,
                                                               const int32_t *dst, int n,
-                                                              const int32_t *count) {
+                                                              const int32_t *count, Rename names) {
   if (count) n = min(n, *count);
+  if constexpr (RENAME) {
+    if ((int)blockIdx.y >= 2 * p.layers) {
+      const int64_t block = blockIdx.x + (int64_t)gridDim.x * blockIdx.z;
+      rename(names, src, dst, n, block * kThreads + threadIdx.x, (int64_t)gridDim.x * gridDim.z * kThreads);
+      return;
+    }
+  }
   const int per_row = p.D / 8, pieces = per_row * p.H * p.S;
   uint16_t *base = ((blockIdx.y & 1) ? p.v : p.k) + (int64_t)(blockIdx.y >> 1) * p.s_layer;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
@@ -71,6 +108,31 @@ __global__ __launch_bounds__(kThreads) void copy_pages_kernel(PageDesc p, const 
       *(u32x4 *)(to + off) = *(const u32x4 *)(from + off);
     }
   }
+}
+
+// n pairs; the renaming, if any, goes with the last launch (launches of 65534
+// planes: the grid's second extent is 16 bits).
+hipError_t copy_pages(const PageDesc &p, const int32_t *src, const int32_t *dst, int n, const int32_t *count,
+                      const Rename *names, hipStream_t s) {
+  if (n == 0) return hipSuccess;
+  const int64_t pieces = (int64_t)p.D / 8 * p.H * p.S;
+  const int x = std::min(n, 1024), z = (int)std::min<int64_t>((pieces + kThreads - 1) / kThreads, 64);
+  constexpr int kMostLayers = 32766;
+  for (int l = 0; l < p.layers; l += kMostLayers) {
+    PageDesc q = p;
+    q.layers = std::min(p.layers - l, kMostLayers);
+    q.k += (int64_t)l * p.s_layer;
+    q.v += (int64_t)l * p.s_layer;
+    if (names && l + q.layers == p.layers)
+      hipLaunchKernelGGL(copy_pages_kernel<true>, dim3(x, 2 * q.layers + 1, z), dim3(kThreads), 0, s, q, src, dst,
+                         n, count, *names);
+    else
+      hipLaunchKernelGGL(copy_pages_kernel<false>, dim3(x, 2 * q.layers, z), dim3(kThreads), 0, s, q, src, dst,
+                         n, count, Rename{});
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // ------------------------------------------------------------ fork and free
@@ -149,6 +211,10 @@ __global__ __launch_bounds__(kPlanThreads) void reserve_kernel(spear_kv_pool_t p
   __shared__ int s_slot[SPEAR_KV_MAX_ENTRIES], s_col[SPEAR_KV_MAX_ENTRIES];
   __shared__ int s_bad;
   const int i = threadIdx.x, S = p.page_size;
+  // the first pages' counts, on their way while the entries are planned
+  int ahead[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) ahead[u] = 4 * i + u < p.num_pages ? p.refs[4 * i + u] : 1;
   if (i == 0) s_bad = 0;
   __syncthreads();
   int slot = -1, have = 0, want = 0, last = -1, held = 0, need = 0;
@@ -199,7 +265,7 @@ __global__ __launch_bounds__(kPlanThreads) void reserve_kernel(spear_kv_pool_t p
     int c = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      f[u] = q + u < p.num_pages && p.refs[q + u] == 0;
+      f[u] = p0 == 0 ? ahead[u] == 0 : q + u < p.num_pages && p.refs[q + u] == 0;
       c += f[u];
     }
     int some;
@@ -262,15 +328,26 @@ __global__ __launch_bounds__(kThreads) void count_used_kernel(const int32_t *ref
 // counted from the lowest.  A used page at q >= U goes to the free page of
 // its rank, which lies below U: both lists have as many entries as there are
 // free pages below U.
+// Without counts every workgroup counts the whole pool itself.
 __global__ __launch_bounds__(kPagesPerBlock) void rank_pages_kernel(
     const int32_t *refs, int P, const int32_t *counts, int blocks, int32_t *src, int32_t *dst,
     int32_t *rank, int32_t *n_moves, int32_t *used) {
   __shared__ int waves[kPlanThreads / 64 + 1];
   int mine = 0, all = 0;  // used pages in the blocks before this one, and in all
-  for (int k = threadIdx.x; k < blocks; k += kPagesPerBlock) {
-    const int c = counts[k];
-    all += c;
-    if (k < (int)blockIdx.x) mine += c;
+  if (counts) {
+    for (int k = threadIdx.x; k < blocks; k += kPagesPerBlock) {
+      const int c = counts[k];
+      all += c;
+      if (k < (int)blockIdx.x) mine += c;
+    }
+  } else {
+#pragma unroll 4
+    for (int k = 0; k < blocks; ++k) {
+      const int q = k * kPagesPerBlock + threadIdx.x;
+      const int c = q < P && refs[q] > 0;
+      all += c;
+      if (k < (int)blockIdx.x) mine += c;
+    }
   }
   int before, U;
   block_scan(mine, before, waves);
@@ -295,30 +372,6 @@ __global__ __launch_bounds__(kPagesPerBlock) void rank_pages_kernel(
   }
 }
 
-// The table's entries and the counts follow their pages.
-__global__ __launch_bounds__(kThreads) void rename_kernel(spear_kv_pool_t p, const int32_t *src,
-                                                          const int32_t *dst, const int32_t *rank,
-                                                          const int32_t *n_moves,
-                                                          const int32_t *used) {
-  const int64_t entries = (int64_t)p.n_slots * p.table_width;
-  const int64_t step = (int64_t)gridDim.x * kThreads;
-  const int U = *used, moves = *n_moves;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < entries; i += step) {
-    const int page = p.table[i];
-    // (an entry that names a page nobody counts is left as it is)
-    if (!in_range(page, p.num_pages) || page < U) continue;
-    const int r = rank[page];
-    if (in_range(r, moves) && src[r] == page) p.table[i] = dst[r];
-  }
-  for (int64_t r = (int64_t)blockIdx.x * kThreads + threadIdx.x; r < moves; r += step) {
-    const int a = src[r], b = dst[r];
-    p.refs[b] = p.refs[a];
-    p.refs[a] = 0;
-  }
-}
-
-int blocks_for(int64_t n, int64_t most) { return (int)std::min<int64_t>((n + kThreads - 1) / kThreads, most); }
-
 }  // namespace
 
 hipError_t launch_kv_append(const AppendDesc &d, hipStream_t s) {
@@ -329,22 +382,8 @@ hipError_t launch_kv_append(const AppendDesc &d, hipStream_t s) {
 }
 
 hipError_t launch_kv_copy_pages(const PageDesc &p, const int32_t *src, const int32_t *dst, int n,
-                                const int32_t *count, hipStream_t s) {
-  if (n == 0) return hipSuccess;
-  const int64_t pieces = (int64_t)p.D / 8 * p.H * p.S;
-  const int z = (int)std::min<int64_t>((pieces + kThreads - 1) / kThreads, 64);
-  const int planes = 2 * p.layers;
-  for (int y0 = 0; y0 < planes; y0 += 65534) {  // the grid's second extent is 16 bits
-    PageDesc q = p;
-    q.k += (int64_t)(y0 / 2) * p.s_layer;
-    q.v += (int64_t)(y0 / 2) * p.s_layer;
-    const int y = std::min(planes - y0, 65534);
-    hipLaunchKernelGGL(copy_pages_kernel, dim3(std::min(n, 1024), y, z), dim3(kThreads), 0, s, q,
-                       src, dst, n, count);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+                                hipStream_t s) {
+  return copy_pages(p, src, dst, n, nullptr, nullptr, s);
 }
 
 hipError_t launch_kv_fork(const spear_kv_pool_t &pool, const int32_t *src, const int32_t *dst,
@@ -375,7 +414,7 @@ hipError_t launch_kv_reserve(const spear_kv_pool_t &pool, const PageDesc &p, con
   hipLaunchKernelGGL(reserve_kernel, dim3(1), dim3(kPlanThreads), 0, s, pool, slots, new_lens, n,
                      missing, taken, move_src, move_dst);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_kv_copy_pages(p, move_src, move_dst, n, nullptr, s);
+  return e != hipSuccess ? e : copy_pages(p, move_src, move_dst, n, nullptr, nullptr, s);
 }
 
 hipError_t launch_kv_compact(const spear_kv_pool_t &pool, const PageDesc &p, int32_t *used,
@@ -383,13 +422,16 @@ hipError_t launch_kv_compact(const spear_kv_pool_t &pool, const PageDesc &p, int
   const int P = pool.num_pages, blocks = (P + kPagesPerBlock - 1) / kPagesPerBlock;
   int32_t *src = pool.scratch, *dst = src + P, *rank = dst + P, *counts = rank + P;
   int32_t *n_moves = counts + blocks;
-  hipLaunchKernelGGL(count_used_kernel, dim3(blocks), dim3(kThreads), 0, s, pool.refs, P, counts);
+  // Up to 32 blocks of pages, counting the pool in every block (128 KB of
+  // counts at most) takes less than a launch of its own.
+  const bool counted = blocks > 32;
+  if (counted)
+    hipLaunchKernelGGL(count_used_kernel, dim3(blocks), dim3(kThreads), 0, s, pool.refs, P, counts);
   hipLaunchKernelGGL(rank_pages_kernel, dim3(blocks), dim3(kPagesPerBlock), 0, s, pool.refs, P,
-                     counts, blocks, src, dst, rank, n_moves, used);
-  hipLaunchKernelGGL(rename_kernel, dim3(blocks_for((int64_t)pool.n_slots * pool.table_width + P, 2048)),
-                     dim3(kThreads), 0, s, pool, src, dst, rank, n_moves, used);
+                     counted ? counts : nullptr, blocks, src, dst, rank, n_moves, used);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_kv_copy_pages(p, src, dst, P, n_moves, s);
+  const Rename names{pool, rank, used};
+  return e != hipSuccess ? e : copy_pages(p, src, dst, P, n_moves, &names, s);
 }
 
 }  // namespace spear

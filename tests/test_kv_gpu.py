@@ -240,3 +240,20 @@ def test_graph_of_a_decode_step():
         for n in ("refs", "table", "lens"):
             assert torch.equal(getattr(a[0], n), getattr(b[0], n)), (i, n)
         new_lens += 1
+
+
+@pytest.mark.parametrize("pages", [32768, 32769, 70000])
+def test_compact_large_pools(pages):
+    """Pools past the size up to which the counts are taken in one launch."""
+    b = Both(pages, 16, 3, 4000, layers=1, heads=1)
+    assert b.reserve([0, 1], [16 * 4000, 16 * 3000]) == 0
+    far = np.random.default_rng(pages).choice(np.arange(7000, pages), 500, replace=False)
+    row = np.full(4000, -1, np.int32)
+    row[:500] = far
+    b.ref._row(2, row)
+    b.ref.lens[2] = 16 * 500
+    for name in ("refs", "table", "lens"):
+        getattr(b.pool, name).copy_(torch.from_numpy(getattr(b.ref, name)))
+    b.free([0])
+    b.compact()
+    b.check("large pool")
