@@ -80,7 +80,11 @@ __device__ void rename(const Rename &n, const int32_t *src, const int32_t *dst, 
 }
 
 // Workgroup (x, layer and array, z): pairs x, x + gridDim.x, ... of one array
-// of one layer, 16 bytes per thread.  RENAME: planes of y past the arrays'
+// of one layer, 16 bytes per thread and step, bound by HBM: 5.4 TB/s of reads
+// and writes for 1.25 GB in 8 layers.  The copies go past the caches (252 ->
+// 237 us there), and so do compaction's sources, each read once (-> 230); a
+// fork's are read once for every child and stay cached (read past the caches
+// 29 -> 42 us for 8 children).  RENAME: planes of y past the arrays'
 // rename the table.
 template <bool RENAME>
 __global__ __launch_bounds__(kThreads) void copy_pages_kernel(PageDesc p, const int32_t *src,
@@ -101,11 +105,13 @@ __global__ __launch_bounds__(kThreads) void copy_pages_kernel(PageDesc p, const 
     if (a == b || !in_range(a, p.num_pages) || !in_range(b, p.num_pages)) continue;
     const uint16_t *from = base + a * p.s_page;
     uint16_t *to = base + b * p.s_page;
+#pragma unroll 4
     for (int j = blockIdx.z * kThreads + threadIdx.x; j < pieces; j += gridDim.z * kThreads) {
       const int row = j / per_row, c = j - row * per_row;
       const int h = row / p.S, s = row - h * p.S;
       const int64_t off = h * p.s_head + s * p.s_token + 8 * c;
-      *(u32x4 *)(to + off) = *(const u32x4 *)(from + off);
+      const u32x4 *at = (const u32x4 *)(from + off);
+      __builtin_nontemporal_store(RENAME ? __builtin_nontemporal_load(at) : *at, (u32x4 *)(to + off));
     }
   }
 }
@@ -116,7 +122,7 @@ hipError_t copy_pages(const PageDesc &p, const int32_t *src, const int32_t *dst,
                       const Rename *names, hipStream_t s) {
   if (n == 0) return hipSuccess;
   const int64_t pieces = (int64_t)p.D / 8 * p.H * p.S;
-  const int x = std::min(n, 1024), z = (int)std::min<int64_t>((pieces + kThreads - 1) / kThreads, 64);
+  const int x = std::min(n, 1024), z = (int)std::min<int64_t>((pieces + 4 * kThreads - 1) / (4 * kThreads), 64);
   constexpr int kMostLayers = 32766;
   for (int l = 0; l < p.layers; l += kMostLayers) {
     PageDesc q = p;
