@@ -364,23 +364,25 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) void attn_decode_kernel(A
           const int h = i / Q4, c = 4 * (i % Q4);
           float M = kNoMax, L = 0.f;
           f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-          for (int k0 = 0; k0 < parts_n; k0 += 8) {
-            f32x4_t po[8], ml[8];
+          constexpr int AT_ONCE = D == 128 ? 16 : 8;  // parts in flight (as registers allow)
+          for (int k0 = 0; k0 < parts_n; k0 += AT_ONCE) {
+            f32x4_t po[AT_ONCE];
+            f32x2_t ml[AT_ONCE];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < AT_ONCE; ++u) {
               const int at = part_at(lead + min(k0 + u, parts_n - 1), h);
+              ml[u] = load_partials2(part_rs, at + D * 4);
               po[u] = load_partials4(part_rs, at + c * 4);
-              ml[u] = load_partials4(part_rs, at + D * 4);
             }
             float M2 = M;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) M2 = fmaxf(M2, ml[u][0]);
+            for (int u = 0; u < AT_ONCE; ++u) M2 = fmaxf(M2, ml[u][0]);
             const float f = __builtin_amdgcn_exp2f(M - M2);
             o *= f;
             L *= f;
             M = M2;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < AT_ONCE; ++u) {
               if (k0 + u >= parts_n) continue;
               const float w = __builtin_amdgcn_exp2f(ml[u][0] - M);
               o += w * po[u];

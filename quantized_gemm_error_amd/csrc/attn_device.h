@@ -168,6 +168,12 @@ __device__ __forceinline__ void load_to_lds(u32x4_t buffer, uint32_t lds, int ev
   }
 }
 
+// Two fp32 values published by another workgroup (as load_partials4).
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ f32x2_t load_partials2(__amdgpu_buffer_rsrc_t r, int byte_off) {
+  return bitcast<f32x2_t>(__builtin_amdgcn_raw_buffer_load_b64(r, byte_off, 0, 16));
+}
+
 // Read-only words at wave-uniform addresses, through the scalar cache: their
 // wait (lgkmcnt) does not drain the vector loads in flight.
 typedef const __attribute__((address_space(4))) int32_t *scalar_i32;
