@@ -713,6 +713,41 @@ def serving_step(torch, device, steps=5):
     return {"chunk": C, "decode_tokens": n_dec, "ec_blocks": sorted(ecs), "step_ms": round(t, 3)}
 
 
+def operators_context(torch, calls):
+    """The cases of perf/operators.py (the paged cache and its attention) through the library:
+    each case's call on three sets of inputs in turn, `calls` of them in one captured graph; the
+    median time of a call over five replays."""
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    out = {}
+    for case in ops.listed():
+        states = [ops.prepare(case, seed) for seed in (1, 2, 3)]
+        for st in states:
+            ops.run(st)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(calls):
+                ops.run(states[i % 3])
+        times = []
+        for rep in range(6):   # the first replay warms up
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b) * 1e3 / calls)
+        us, work = sorted(times[1:])[2], ops.work(case)
+        out[case["name"]] = {"us": round(us, 2), "GB/s": round(work["bytes"] / us / 1e3, 1),
+                             "TFLOP/s": round(work["flops"] / us / 1e6, 1)}
+        del graph, states
+        torch.cuda.empty_cache()
+    return out
+
+
 def ceilings(torch, device):
     """Context only: a 1 GiB device-to-device copy, and hipBLASLt bf16 GEMMs at the prefill
     shapes (dense bf16 weights, torch.matmul)."""
@@ -993,7 +1028,8 @@ LAYER_CMDS = {
     "fetch": "rocprofv3 --pmc FETCH_SIZE -f csv -d gpurun_out/prof_{tag}_fetch -o run -- python3 bench.py {mode} --copy-calibration",
     "write": "rocprofv3 --pmc WRITE_SIZE -f csv -d gpurun_out/prof_{tag}_write -o run -- python3 bench.py {mode} --copy-calibration",
 }
-LAYER_MODES = {"llama70b_layer": "--llama70b-only", "serving_step_7b": "--serving-step"}
+LAYER_MODES = {"llama70b_layer": "--llama70b-only", "serving_step_7b": "--serving-step",
+               "attention_kernels": "--operators 10"}
 
 
 def summarize_layer_profiles(tag, title, trace_dir, fetch_dir, write_dir, out_dir):
@@ -1010,7 +1046,7 @@ def summarize_layer_profiles(tag, title, trace_dir, fetch_dir, write_dir, out_di
     trace = rows(os.path.join(trace_dir, "run_kernel_trace.csv"))
     dur = {}
     for r in trace:
-        if r["Kernel_Name"].startswith("__amd_rocclr") or "at::" in r["Kernel_Name"]:
+        if r["Kernel_Name"].startswith("__amd_rocclr") or "at::" in r["Kernel_Name"] or "rocprim" in r["Kernel_Name"]:
             continue   # copies and the set-up's torch kernels
         grid = int(r["Grid_Size_X"]) * int(r["Grid_Size_Y"]) * int(r["Grid_Size_Z"])
         key = (_short(r["Kernel_Name"]), grid)
@@ -1173,6 +1209,9 @@ def main():
     ap.add_argument("--serving-only", action="store_true",
                     help="run only the serving-stack leg (latency table, chunk selector, request "
                          "stream) and print it")
+    ap.add_argument("--operators", type=int, metavar="CALLS",
+                    help="time only the paged cache's operators and its attention (the cases of "
+                         "perf/operators.py), CALLS calls of each in a graph, and print them")
     args = ap.parse_args()
     if args.summarize_profiles:
         summarize_profiles(*args.summarize_profiles, out_dir=os.path.join(ROOT, "profiles"))
@@ -1201,9 +1240,10 @@ def main():
     if args.serving_only:
         print(json.dumps({"serving_stack_7b": serving_context(torch, dev)}), flush=True)
         return
-    if args.llama70b_only or args.serving_step:
+    if args.llama70b_only or args.serving_step or args.operators:
         out = ({"llama70b_layer_fp16": llama70b_context(torch, dev)} if args.llama70b_only
-               else {"serving_step": serving_step(torch, dev)})
+               else {"serving_step": serving_step(torch, dev)} if args.serving_step
+               else {"operators": operators_context(torch, args.operators)})
         if args.copy_calibration:   # the reference copies that scale the byte counters
             src = torch.empty(COPY_CAL_BYTES, dtype=torch.uint8, device=dev).fill_(1)
             dst = torch.empty_like(src)

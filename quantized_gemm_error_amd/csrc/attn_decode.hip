@@ -24,17 +24,28 @@
 //     groups read four whole rows at once), and pairs of keys are interleaved
 //     in registers (v_perm): row r of product j is dim D/16 r + j.
 // The matrix units do at most 16/G times the needed work and are still idle
-// most of the time (per 32 keys and wave 256 cycles of MFMA at D = 128).
+// most of the time (per 32 keys and wave 256 cycles of MFMA at D = 128).  The
+// weights are rounded to the type once, for the second product; with random
+// values that adds less than the output's own rounding (error against 64 bits
+// 0.0019 with it, 0.0017 without, bf16).
 //
 // The work of a head is one list: the 32-key tiles that the sequences' queries
 // see, one sequence after the other.  It is cut into R equal runs, whatever the
 // lengths, R such that the workgroups (R runs x heads) all run at once, and
 // the heads go through it in step, which keeps the reads of one moment in the
-// same pages.  A workgroup's waves stream through their run without a pause:
-// the next tile's loads are issued before the present one's products, across
-// the ends of sequences too.  Where a run ends inside a sequence, the parts
-// meet in the workspace and the workgroup that completes them joins them in
-// list order.
+// same pages (one list over heads and sequences: 212 us where this takes 190).
+// A workgroup's waves stream through their run without a pause: the next
+// tile's loads are issued before the present one's products, across the ends
+// of sequences too.  Where a run ends inside a sequence, the parts meet in the
+// workspace and the workgroup that completes them joins them in list order.
+//
+// Measured (MI355X, graph-replayed): 32 rows of 32 heads over 512..4144 keys
+// 190 us for 1.22 GB (6.4 TB/s; a device copy reaches 5.2), 4 rows of 64 / 8
+// heads over up to 32768 keys 79 us (5.7 TB/s), 48 rows in windows of 4096 in
+// token-major pages 138 us (5.4 TB/s), one row over 257 keys 6.1 us.
+// Tried: four-wave workgroups, three to a CU, 230 us; 128 registers at D = 128
+// for twice the waves 344 us (spills); K past the caches too 166 -> 180 us for
+// the windowed rows (its 64-byte pieces of a row come by two instructions).
 #include <algorithm>
 
 #include "attn_device.h"
@@ -44,7 +55,10 @@ namespace spear {
 namespace {
 
 constexpr int kTile = 32;      // keys a wave takes at a time
-constexpr int kMinTiles = 16;  // a workgroup's share of the list is no less
+// Short calls: no less than this to a workgroup, two tiles a wave.  Measured: 8
+// instead of 16 costs a row over 257 keys 2 us more and one over 8192 keys 3,
+// for the joins; 32 takes 3 to 5 us more for one to four rows over 2048 to 8192.
+constexpr int kMinTiles = 16;
 
 // What a sequence's query sees as a list of 32-key tiles: `sink_tiles` from
 // position 0, then those from lo_tile on.
