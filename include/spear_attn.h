@@ -34,7 +34,8 @@ extern "C" {
  * larger one.
  *   head_dim    64 or 128.
  *   page_size   a multiple of 16, at most 65536.
- *   strides     multiples of 8; no two elements may share an address.
+ *   strides     multiples of 8; no two elements may share an address; one
+ *               layer's page spans at most 2^29 elements.
  *   k, v        16-byte aligned.
  * A multi-token call may address past 2^31 elements; offsets are 64-bit.
  * The attention and append calls take one layer (n_layers == 1: offset k and
@@ -60,7 +61,8 @@ typedef struct spear_kv_cache {
  *                per sequence.  Sequences without new tokens are fine.
  *   n_tokens     rows of q (n_seqs when q_starts is NULL).  Rows that no
  *                sequence covers are left as they are.
- * n_seqs <= SPEAR_ATTN_MAX_SEQS.  A table entry outside 0..num_pages-1 hides the tokens of its page.
+ * n_seqs <= SPEAR_ATTN_MAX_SEQS, n_tokens <= 2^24 (times n_q_heads: 2^30),
+ * table_width * page_size <= 2^30 (times n_seqs: 2^35).  A table entry outside 0..num_pages-1 hides the tokens of its page.
  */
 #define SPEAR_ATTN_MAX_SEQS 4096
 typedef struct spear_kv_batch {
@@ -99,12 +101,13 @@ typedef struct spear_attn_args {
 /*
  * Workspace bytes that spear_attn_decode and spear_attn_prefill need for this
  * cache and number of query heads with at most n_seqs sequences and n_tokens
- * rows; 0 when an argument is invalid.  256-byte aligned, ZEROED ONCE before
- * its first use, left ready by every call; any attention call of at most
- * these sizes may use it.  It is not interchangeable with
+ * rows; 0 when an argument is invalid.  256-byte aligned, its first
+ * SPEAR_ATTN_HEADER_BYTES ZEROED ONCE before its first use, left ready by
+ * every call; any attention call of at most these sizes may use it.  It is not interchangeable with
  * spear_workspace_bytes' workspace.  Calls that may overlap need different
  * ones.
  */
+#define SPEAR_ATTN_HEADER_BYTES 16384
 size_t spear_attn_workspace_bytes(const spear_kv_cache_t *cache, int32_t n_q_heads,
                                   int32_t n_seqs, int32_t n_tokens);
 

@@ -18,6 +18,7 @@ from .spear import SpearError, _check, _require, SPEAR_ERR_INVALID_ARGUMENT
 
 SPEAR_ATTN_MAX_SEQS = 4096
 SPEAR_KV_MAX_ENTRIES = 1024
+SPEAR_ATTN_HEADER_BYTES = 16384
 
 # Every function the header declares, for the export check.
 EXPORTED = (
@@ -237,13 +238,14 @@ def spear_attn_workspace_bytes(cache: SpearKVCache, n_q_heads: int, n_seqs: int,
 
 
 def new_attn_workspace(cache: SpearKVCache, n_q_heads: int, n_seqs: int, n_tokens: int):
-    """A zeroed, 256-byte aligned workspace for attention calls of at most these sizes."""
+    """A 256-byte aligned workspace with a zeroed header for attention calls of at most these sizes."""
     import torch
     n = spear_attn_workspace_bytes(cache, n_q_heads, n_seqs, n_tokens)
     if n == 0:
         raise SpearError(SPEAR_ERR_INVALID_ARGUMENT, spear.spear_last_error())
-    buf = torch.zeros(n + 256, dtype=torch.uint8, device=cache.device)
+    buf = torch.empty(n + 256, dtype=torch.uint8, device=cache.device)
     off = (-buf.data_ptr()) % 256
+    buf[off:off + SPEAR_ATTN_HEADER_BYTES].zero_()
     return buf[off:off + n]
 
 

@@ -78,8 +78,8 @@ spear_status_t check_cache(const spear_kv_cache_t *c, bool one_layer) {
     return fail(SPEAR_ERR_INVALID_ARGUMENT, "cache strides make elements share addresses");
   // offsets inside a page are 32-bit in the kernels
   if ((c->n_kv_heads - 1) * c->stride_head + (c->page_size - 1) * c->stride_token + c->head_dim >
-      (int64_t(1) << 30))
-    return fail(SPEAR_ERR_UNSUPPORTED, "a page spans more than 2^30 elements");
+      (int64_t(1) << 29))
+    return fail(SPEAR_ERR_UNSUPPORTED, "a page of a layer spans more than 2^29 elements");
   return SPEAR_OK;
 }
 

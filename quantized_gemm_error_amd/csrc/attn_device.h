@@ -123,6 +123,13 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
   return ((x & kExp<DT>) + kExpOne<DT>) & 0x80008000u;
 }
 
+// This wave's loads to LDS have landed (vmcnt(0)); no LDS read moves before it.
+__device__ __forceinline__ void wait_for_lds_loads() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // A buffer of `bytes` bytes at p, both wave-uniform, as its descriptor words.
@@ -136,7 +143,7 @@ __device__ __forceinline__ u32x4_t buffer_words(const void *p, int bytes) {
 // byte j step + (j odd ? odd : even), to LDS byte lds + 1024 j + 16 i (lds and
 // step are wave-uniform).  Bytes past the buffer's range read as zeros.
 // Written out because the compiler waits for every such load before any later
-// LDS read; the caller waits (vmcnt) before a barrier instead.  The block
+// LDS read; the caller waits (wait_for_lds_loads) before a barrier instead.  The block
 // writes no register but m0, which nothing else in these kernels uses; the
 // wait states are those of a scalar register that a vector instruction may
 // have written just before (the first load) and of m0.
@@ -186,5 +193,6 @@ __device__ __forceinline__ int scalar_load(const int32_t *p, int64_t i) {
 // writes before it reads it lies past it.
 constexpr int kAttnCounters = 4096;
 constexpr size_t kAttnDataOff = kAttnCounters * sizeof(uint32_t);
+static_assert(kAttnDataOff == SPEAR_ATTN_HEADER_BYTES, "the header that the caller zeroes");
 
 }  // namespace spear

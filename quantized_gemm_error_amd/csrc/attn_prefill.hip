@@ -105,7 +105,7 @@ constexpr int kJoinRows = 100;   // rows of partial sums that are joined in the 
 constexpr int kMaxParts = 63;
 constexpr int kWhole = 1 << 29;  // tiles per part: no block is cut
 
-__device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_rows, int extra_items,
+__device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_rows, int most_items,
                                           Item &k) {
   const int lane = threadIdx.x & 63;
   struct Seq {
@@ -140,7 +140,7 @@ __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_row
   const int blocks = sum([](const Seq &s) { return min(s.blocks, 1 << 18); });
   const int slots = max(kSlots / d.Hkv, 1);
   int per = kWhole;
-  if (blocks <= kAttnCounters / d.Hkv && extra_items > 0) {
+  if (blocks <= kAttnCounters / d.Hkv && blocks < most_items) {
     const int total = sum([](const Seq &s) { return s.total; });
     int most = mine.longest;
     for (int b0 = 64; b0 < d.n_seqs; b0 += 64) most = max(most, seq_of(b0 + lane).longest);
@@ -167,7 +167,7 @@ __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_row
       }
       join = (wave_max(join) + kJoinRows - 1) / kJoinRows;
       const int cost = kPartTiles + join + (items <= slots ? p : even + (p + 1) / 2);
-      if (rows <= part_rows && items <= blocks + extra_items && cost < least) {
+      if (rows <= part_rows && items <= most_items && cost < least) {
         least = cost;
         per = p;
       }
@@ -212,7 +212,7 @@ __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_row
 }
 
 template <int DT, int D>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d, int part_rows, int extra_items,
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d, int part_rows, int most_items,
                                                                      uint32_t *counters, float *parts,
                                                                      int part_bytes) {
   constexpr int CH = D / 8;          // 16-byte chunks of a row
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   const int col = lane & 31, half = lane >> 5;
   const int kvh = blockIdx.x % d.Hkv;
   Item blk;
-  if (!find_item(d, blockIdx.x / d.Hkv, part_rows, extra_items, blk)) return;
+  if (!find_item(d, blockIdx.x / d.Hkv, part_rows, most_items, blk)) return;
   blk = {uniform(blk.b), uniform(blk.start), uniform(blk.n), uniform(blk.row0), uniform(blk.part),
          uniform(blk.parts), uniform(blk.part_row), uniform(blk.block)};
 
@@ -355,7 +355,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   if (tiles > 0) {
     Source now = source_of(0), next = now;
     load_keys(now, lds);
-    __builtin_amdgcn_s_waitcnt(0x0F70);
+    wait_for_lds_loads();
     lds_barrier();
     load_values(now, lds + 2 * TILE);
     if (tiles > 1) {
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
       const int key0 = key_of(t);
       const char *kt = s_kv[buf ^ 1], *vt = s_kv[2 + buf];
       const bool masked = partly(key0, p_min, p_max);
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's parts are in LDS
+      wait_for_lds_loads();  // this wave's parts of V(t) and K(t + 1)
       int flags = now.bytes == kHidden ? 1 : 0;
       if (masked) {  // (only V: a score that is no number is replaced, a weight of 0 is not)
         uint32_t bad = 0;
@@ -647,7 +647,7 @@ hipError_t launch_attn_prefill(const AttnDesc &d, void *ws, hipStream_t s) {
   const int64_t items = blocks + extra;
   auto *k = d.D == 64 ? (d.dtype == DT_F16 ? attn_prefill_kernel<DT_F16, 64> : attn_prefill_kernel<DT_BF16, 64>)
                       : (d.dtype == DT_F16 ? attn_prefill_kernel<DT_F16, 128> : attn_prefill_kernel<DT_BF16, 128>);
-  hipLaunchKernelGGL(k, dim3((unsigned)(items * d.Hkv)), dim3(64 * kWaves), 0, s, d, part_rows, extra,
+  hipLaunchKernelGGL(k, dim3((unsigned)(items * d.Hkv)), dim3(64 * kWaves), 0, s, d, part_rows, extra > 0 ? (int)items : 0,
                      (uint32_t *)ws, (float *)((char *)ws + kAttnDataOff),
                      (int)((size_t)part_rows * d.Hkv * (d.D + 4) * sizeof(float)));
   return hipGetLastError();

@@ -61,6 +61,7 @@ BAD_CACHES = [
     (dict(stride_token=60), INVALID), (dict(stride_page=0), INVALID), (dict(stride_head=64), INVALID),
     (dict(stride_page=2 * 16 * 64 - 8), INVALID), (dict(stride_token=-64), INVALID),
     (dict(stride_page=1 << 62), INVALID),
+    (dict(stride_token=1 << 26, stride_page=1 << 32, stride_head=64), UNSUPPORTED),
 ]
 
 
@@ -79,7 +80,7 @@ def test_cache_refusals(lib, kw, status):
     (dict(n_seqs=-1), INVALID), (dict(table_width=0), INVALID), (dict(n_tokens=-1), INVALID),
     (dict(n_tokens=4), INVALID), (dict(block_table=None), INVALID), (dict(kv_lens=None), INVALID),
     (dict(kv_lens=(1 << 35) + 2), INVALID), (dict(n_seqs=5000, n_tokens=5000), UNSUPPORTED),
-    (dict(table_width=1 << 27), UNSUPPORTED),
+    (dict(table_width=1 << 27), UNSUPPORTED), (dict(n_seqs=4096, n_tokens=4096, table_width=1 << 20), UNSUPPORTED),
 ])
 def test_batch_refusals(lib, kw, status):
     b = _batch(**kw)
@@ -99,6 +100,14 @@ def test_batch_refusals(lib, kw, status):
 def test_argument_refusals(lib, kw, status):
     for fn in (lib.spear_attn_decode, lib.spear_attn_prefill):
         assert fn(R(_cache()), R(_batch()), R(_args(**kw)), None, 0, None) == status
+
+
+def test_too_many_rows(lib):
+    b = _batch(n_tokens=1 << 24, q_starts=1 << 39)
+    c = _cache(n_kv_heads=1, stride_head=0)
+    assert lib.spear_attn_prefill(R(c), R(b), R(_args(n_q_heads=128)), None, 0, None) == UNSUPPORTED
+    b = _batch(n_tokens=(1 << 24) + 1, q_starts=1 << 39)
+    assert lib.spear_kv_append(R(c), R(b), 1 << 36, 1 << 37, 128, 64, 128, 64, None) == UNSUPPORTED
 
 
 def test_null_structs_layers_and_q_starts(lib):

@@ -295,6 +295,40 @@ def test_offsets_past_32_bits():
         check(out, lse, reference(cc, 1 / math.sqrt(128), 0, 0), cc, 1 / math.sqrt(128), "far pages")
 
 
+@pytest.mark.parametrize("heads", [(2, 2), (8, 1)])
+def test_many_short_sequences(heads):
+    """More sequences than a few waves' lanes, of none, one and a few new tokens."""
+    rng = np.random.default_rng(heads[0])
+    lens = [int(n) for n in rng.integers(0, 70, 600)]
+    lens[77], lens[400] = 2000, 1300
+    c = make_case(5, lens, heads, 64, 16, "f16")
+    verify(c, "decode, 600 sequences")
+    c = make_case(6, lens, heads, 64, 16, "bf16", [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 4, 600))])
+    verify(c, "chunks, 600 sequences")
+    verify(c, "chunks, 600 sequences, window", window=20, sinks=3)
+
+
+def test_rows_of_no_sequence_are_left_alone():
+    c = make_case(7, [40, 60], (4, 2), 64, 16, "f16", [10, 20])
+    q = torch.cat([c.q, c.q[:5]]).cuda()  # five rows past q_starts' end
+    out = torch.full_like(q, 9.0)
+    run(c, q=q, out=out, lse=False)
+    check(out[:30], None, reference(c, 1 / 8, 0, 0), c, 1 / 8, "covered rows")
+    assert (out[30:] == 9).all()
+
+
+@pytest.mark.parametrize("starts", [[0, 50, 20], [7, 3, 1 << 30], [-5, 10, 99], [0, 0, -1], [1 << 30, 5, 30]])
+def test_q_starts_out_of_order_stay_inside(starts):
+    """Nothing outside the tensors is touched: what lies beside q and out keeps its values."""
+    c = make_case(7, [40, 60], (4, 2), 64, 16, "f16", [10, 20])
+    c.starts = starts
+    frame = torch.full((90, 4, 64), 5.0, dtype=torch.float16, device="cuda")
+    out = frame[30:60]
+    run(c, out=out, lse=False)
+    torch.cuda.synchronize()
+    assert (frame[:30] == 5).all() and (frame[60:] == 5).all()
+
+
 def test_no_rows_and_no_sequences():
     c = make_case(1, [5, 9], (4, 2), 64, 16, "f16", [0, 0])
     out, lse = run(c)
