@@ -7,7 +7,8 @@
 // relative rounding is the same); out = o / l, lse = ln 2 (m + log2 l).
 //
 // The work is two matrix products, 4 D flops per visible pair, so MFMA bounds
-// it.  A workgroup of four waves owns 128 rows of one key-value head: the
+// it.  A group of four waves owns 128 rows of one key-value head (a workgroup is
+// one group or two, chosen at the launch): the
 // query heads of a token that share it are neighbouring rows (row = token x
 // G + head), so short chunks of grouped heads fill tiles too and share every
 // staged key.  Each wave takes 32 rows with 32x32x16 MFMAs, transposed so that
@@ -52,7 +53,7 @@ namespace {
 
 constexpr int kRows = 128;  // query rows of a workgroup
 constexpr int kKeys = 64;   // keys of a tile
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;   // of 32 rows each
 constexpr float kSlack = 8.f;  // by how much a maximum may pass m
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
@@ -98,13 +99,14 @@ struct Item {
 // otherwise the tiles and the starts and joins of the parts spread over the
 // slots, and half a part more at the end; the cheapest of a few sizes is
 // taken, whole blocks among them.
-constexpr int kSlots = 512;      // workgroups that run at once: two to a CU
+constexpr int kSlots = 512;      // groups of four waves that run at once: two to a CU
 constexpr int kMinTiles = 4;     // of a part
-constexpr int kPartTiles = 3;    // what a part's start and its partial sums cost, in tiles
-constexpr int kJoinRows = 100;   // rows of partial sums that are joined in the time of a tile
+constexpr int kPartTiles = 3;    // what a part's start and its partial sums cost, in tiles of a group
+constexpr int kJoinRows = 100;   // rows of partial sums that are joined in the time of one
 constexpr int kMaxParts = 63;
 constexpr int kWhole = 1 << 29;  // tiles per part: no block is cut
 
+template <int GROUPS>
 __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_rows, int most_items,
                                           Item &k) {
   const int lane = threadIdx.x & 63;
@@ -138,7 +140,7 @@ __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_row
   // (sums that device data of any kind cannot overflow: each term is bounded
   // by more than a whole cut batch may have)
   const int blocks = sum([](const Seq &s) { return min(s.blocks, 1 << 18); });
-  const int slots = max(kSlots / d.Hkv, 1);
+  const int slots = max(kSlots / GROUPS / d.Hkv, 1);
   int per = kWhole;
   if (blocks <= kAttnCounters / d.Hkv && blocks < most_items) {
     const int total = sum([](const Seq &s) { return s.total; });
@@ -165,8 +167,8 @@ __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_row
         const int parts = s.blocks > 0 ? parts_of(s, p) : 1;
         join = max(join, parts > 1 ? parts * min(s.n * d.G, kRows) : 0);
       }
-      join = (wave_max(join) + kJoinRows - 1) / kJoinRows;
-      const int cost = kPartTiles + join + (items <= slots ? p : even + (p + 1) / 2);
+      join = (wave_max(join) * GROUPS + kJoinRows - 1) / kJoinRows;
+      const int cost = GROUPS * kPartTiles + join + (items <= slots ? p : even + (p + 1) / 2);
       if (rows <= part_rows && items <= most_items && cost < least) {
         least = cost;
         per = p;
@@ -177,7 +179,7 @@ __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_row
   // The last items, which see the most keys, come first; of up to two
   // workgroups a CU, the second ones, which a launch places after every CU has
   // one, go the other way, so that CUs get like amounts of work.
-  const int first_round = max(slots / 2, 1);
+  const int first_round = max(kSlots / 2 / d.Hkv, 1);
   if (w >= items) return false;
   w = w < first_round || items > 2 * first_round ? items - 1 - w : w - first_round;
   int before = 0, rows_before = 0, blocks_before = 0;
@@ -211,10 +213,12 @@ __device__ __forceinline__ bool find_item(const AttnDesc &d, int w, int part_row
   return false;
 }
 
-template <int DT, int D>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d, int part_rows, int most_items,
-                                                                     uint32_t *counters, float *parts,
-                                                                     int part_bytes) {
+// GROUPS: groups of four waves.  With two, both have the same rows, with
+// buffers of their own, and take the part's tiles by turns; the second's sums
+// then join the first's through LDS.
+template <int DT, int D, int GROUPS>
+__global__ __launch_bounds__(64 * kWaves * GROUPS, 2) void attn_prefill_kernel(
+    AttnDesc d, int part_rows, int most_items, uint32_t *counters, float *parts, int part_bytes) {
   constexpr int CH = D / 8;          // 16-byte chunks of a row
   constexpr int KS = D / 16;         // contraction steps of S
   constexpr int DB = D / 32;         // 32-dim blocks of O
@@ -222,14 +226,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   constexpr int LOADS = 16 / RPI;    // instructions for 16 keys
   constexpr int TILE = kKeys * D * 2;  // bytes of a staged K or V tile
   static_assert((kMaxParts + 1) * kRows * 4 <= 4 * TILE, "the join's weights");
-  __shared__ __attribute__((aligned(256))) char s_kv[4][TILE];  // K tiles of even and odd t, then V's
-  __shared__ __attribute__((aligned(16))) int s_flags[2][kWaves];  // of a tile's 16-key groups: 1 hidden, 2 not finite
+  static_assert(GROUPS == 1 || kRows * (D + 4) * 4 <= 8 * TILE, "a group's sums");
+  constexpr int THREADS = 64 * kWaves * GROUPS;
+  // of a group: K tiles of its even and odd t, then V's
+  __shared__ __attribute__((aligned(256))) char s_all[GROUPS][4][TILE];
+  // of a group's tile, by 16 keys: 1 hidden, 2 not finite
+  __shared__ __attribute__((aligned(16))) int s_flags[2][GROUPS][kWaves];
 
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = GROUPS == 1 ? wave_all : wave_all % kWaves;  // in its group
+  const int team = GROUPS == 1 ? 0 : wave_all / kWaves;
+  char (&s_kv)[4][TILE] = s_all[team];
   const int col = lane & 31, half = lane >> 5;
   const int kvh = blockIdx.x % d.Hkv;
   Item blk;
-  if (!find_item(d, blockIdx.x / d.Hkv, part_rows, most_items, blk)) return;
+  if (!find_item<GROUPS>(d, blockIdx.x / d.Hkv, part_rows, most_items, blk)) return;
   blk = {uniform(blk.b), uniform(blk.start), uniform(blk.n), uniform(blk.row0), uniform(blk.part),
          uniform(blk.parts), uniform(blk.part_row), uniform(blk.block)};
 
@@ -246,12 +258,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   const int w_end = min(wrow0 + 32, all_rows);
   const int w_min = past + wrow0 / d.G, w_max = past + (w_end - 1) / d.G;
 
-  // the part's tiles, counted from the part's first
+  // the part's tiles, of which this group has every GROUPS-th
   const Tiles list(d, p_min, p_max);
   const int first = blk.parts == 1 ? 0 : (int)((int64_t)list.count * blk.part / blk.parts);
-  const int tiles = (blk.parts == 1 ? list.count : (int)((int64_t)list.count * (blk.part + 1) / blk.parts)) - first;
+  const int part_tiles =
+      (blk.parts == 1 ? list.count : (int)((int64_t)list.count * (blk.part + 1) / blk.parts)) - first;
+  const auto of_group = [&](int n) { return max(n + GROUPS - 1 - team, 0) / GROUPS; };
+  const int tiles = of_group(part_tiles), steps = (part_tiles + GROUPS - 1) / GROUPS;
   const auto key_of = [&](int t) {
-    t += first;
+    t = first + GROUPS * t + team;
     return kKeys * (t < list.sink_tiles ? t : t - list.sink_tiles + list.lo_tile);
   };
 
@@ -351,13 +366,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   // The tiles that some row of this wave sees are the first w_tiles (those
   // that a window hides from all of its rows are computed and masked).
   const int w_tiles =
-      !active || w_max < 0 ? 0 : min(tiles, list.count - (p_max / kKeys - w_max / kKeys) - first);
-  if (tiles > 0) {
-    Source now = source_of(0), next = now;
-    load_keys(now, lds);
+      !active || w_max < 0
+          ? 0
+          : of_group(min(part_tiles, max(list.count - (p_max / kKeys - w_max / kKeys) - first, 0)));
+  if (steps > 0) {
+    Source now{0, 0};
+    if (tiles > 0) {
+      now = source_of(0);
+      load_keys(now, lds);
+    }
+    Source next = now;
     wait_for_lds_loads();
     lds_barrier();
-    load_values(now, lds + 2 * TILE);
+    if (tiles > 0) load_values(now, lds + 2 * TILE);
     if (tiles > 1) {
       next = source_of(1);
       load_keys(next, lds + TILE);
@@ -373,7 +394,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
     const auto tile = [&](const int t, const int buf, f32x16_t (&s)[2], f32x16_t (&ahead)[2]) {
       const int key0 = key_of(t);
       const char *kt = s_kv[buf ^ 1], *vt = s_kv[2 + buf];
-      const bool masked = partly(key0, p_min, p_max);
+      const bool masked = (GROUPS == 1 || t < tiles) && partly(key0, p_min, p_max);
       wait_for_lds_loads();  // this wave's parts of V(t) and K(t + 1)
       int flags = now.bytes == kHidden ? 1 : 0;
       if (masked) {  // (only V: a score that is no number is replaced, a weight of 0 is not)
@@ -386,10 +407,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
         }
         flags |= __any(bad != 0) ? 2 : 0;
       }
-      if (lane == 0) s_flags[buf][wave] = flags;
+      if (lane == 0) s_flags[buf][team][wave] = flags;
       lds_barrier();
       // (first the reads whose latency the loads' issue covers)
-      const u32x4_t group = *(const u32x4_t *)s_flags[buf];
+      const u32x4_t group = *(const u32x4_t *)s_flags[buf][team];
+      u32x4_t either = group;
+      if constexpr (GROUPS == 2) either |= *(const u32x4_t *)s_flags[buf][team ^ 1];
       u32x4_t kf[AHEAD], vf[AHEAD];
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) kf[i] = k_frag(kt, i);
@@ -399,12 +422,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
         next = source_of(t + 2);
         load_keys(next, lds + buf * TILE);
       }
-      const int any = uniform((int)(group[0] | group[1] | group[2] | group[3]));
-      const bool dirty = any & 2;
+      const int any = uniform((int)(either[0] | either[1] | either[2] | either[3]));
+      const bool dirty = any & 2;  // (of either group: the path has barriers)
       const bool mine = t < w_tiles;
       if (!mine && !dirty) return;
+      // a tile that no row sees is masked as any other; past the group's last
+      // there is none
+      const bool looks = GROUPS == 1 || mine;
 
-      if ((any & 1) || partly(key0, w_min, w_max)) {
+      if (looks && ((any & 1) || partly(key0, w_min, w_max))) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -420,7 +446,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int v = 0; v < 16; ++v) top = fmaxf(top, s[u][v]);
-      if (__any(top > m + slack)) {
+      if (looks && __any(top > m + slack)) {
         top = over_halves(top, [](float a, float b) { return fmaxf(a, b); });
         const float m2 = fmaxf(m, top), f = __builtin_amdgcn_exp2f((m - m2) * scale);
         m = m2;
@@ -437,7 +463,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
         // the tile.
         constexpr uint32_t kOnes = DT == DT_F16 ? 0x3C003C00u : 0x3F803F80u;
 #pragma unroll 1
-        for (int sign = 0; sign < 2; ++sign) {
+        for (int sign = looks ? 0 : 2; sign < 2; ++sign) {
           const uint32_t flip = sign ? 0x80008000u : 0u;
 #pragma unroll
           for (int b = 0; b < DB; ++b) {
@@ -518,10 +544,41 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
       __builtin_amdgcn_s_setprio(0);
       l += sum[0] + sum[1];
     };
-    for (int t = 0; t < tiles; t += 2) {
+    for (int t = 0; t < steps; t += 2) {
       tile(t, 0, s_even, s_odd);
-      if (t + 1 < tiles) tile(t + 1, 1, s_odd, s_even);
+      if (t + 1 < steps) tile(t + 1, 1, s_odd, s_even);
     }
+  }
+  if constexpr (GROUPS == 2) {  // the second group's sums join the first's
+    float *at = (float *)s_all + (32 * wave + col) * (D + 4);
+    lds_barrier();
+    if (team == 1) {
+#pragma unroll
+      for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int v = 0; v < 16; v += 4)
+          *(f32x4_t *)(at + 32 * b + 2 * v + 4 * half) =
+              f32x4_t{acc[b][v], acc[b][v + 1], acc[b][v + 2], acc[b][v + 3]};
+      at[D + half] = l;  // (a half's l: the other half has the other keys')
+      if (half == 0) at[D + 2] = m;
+    }
+    lds_barrier();
+    if (team == 0) {
+      const float m1 = at[D + 2], m2 = fmaxf(m, m1);
+      const float f0 = __builtin_amdgcn_exp2f((m - m2) * scale), f1 = __builtin_amdgcn_exp2f((m1 - m2) * scale);
+      m = m2;
+      l = f0 * l + f1 * at[D + half];
+#pragma unroll
+      for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int v = 0; v < 16; v += 4) {
+          const f32x4_t x = *(const f32x4_t *)(at + 32 * b + 2 * v + 4 * half);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[b][v + i] = f0 * acc[b][v + i] + f1 * x[i];
+        }
+    }
+    if (blk.parts == 1 && team == 1) return;
+    lds_barrier();  // (with parts, the sums' LDS is used again)
   }
   l = over_halves(l, [](float a, float b) { return a + b; });
   const auto store = [&](int r, f32x4_t o, int c, float lse) {  // dims c.. of row r
@@ -550,7 +607,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   const auto part_at = [&](int part, int r) {  // byte offset of a row's part
     return (kvh * part_rows + blk.part_row + part * all_rows + r) * (D + 4) * 4;
   };
-  if (is_row) {
+  if (is_row && team == 0) {
     const int at = part_at(blk.part, row);
 #pragma unroll
     for (int b = 0; b < DB; ++b)
@@ -562,17 +619,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   lds_barrier();
   uint32_t *counter = counters + blk.block * d.Hkv + kvh;
   if (threadIdx.x == 0)
-    s_flags[0][0] = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+    s_flags[0][0][0] = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                     (uint32_t)blk.parts - 1;
   lds_barrier();
-  if (!s_flags[0][0]) return;
+  if (!s_flags[0][0][0]) return;
   if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   // First each row's weights of the parts, w_s = 2^((m_s - M) scale) / L, and
   // M and L; then the sums, with many loads in flight.  LDS is free by now.
   const int rows = min(kRows, all_rows - blk.row0);
-  float *w_of = (float *)s_kv[0];             // [kMaxParts][kRows]
+  float *w_of = (float *)s_all;               // [kMaxParts][kRows]
   float *lse_of = w_of + kMaxParts * kRows;   // [kRows]
-  for (int r = threadIdx.x; r < rows; r += 64 * kWaves) {
+  for (int r = threadIdx.x; r < rows; r += THREADS) {
     float M = kNoMax, L = 0.f;
     for (int k0 = 0; k0 < blk.parts; k0 += 8) {
       f32x4_t ml[8];
@@ -595,12 +652,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
   }
   lds_barrier();
   constexpr int AT_ONCE = 4, Q4 = D / 4;
-  for (int i0 = threadIdx.x; i0 < rows * Q4; i0 += AT_ONCE * 64 * kWaves) {
+  for (int i0 = threadIdx.x; i0 < rows * Q4; i0 += AT_ONCE * THREADS) {
     f32x4_t o[AT_ONCE];
     int r[AT_ONCE], at[AT_ONCE];
 #pragma unroll
     for (int j = 0; j < AT_ONCE; ++j) {  // (past the last row: the last row again, not stored)
-      const int i = min(i0 + j * 64 * kWaves, rows * Q4 - 1);
+      const int i = min(i0 + j * THREADS, rows * Q4 - 1);
       r[j] = i / Q4;
       at[j] = 16 * (i % Q4);
       o[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -620,7 +677,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(AttnDesc d
     }
 #pragma unroll
     for (int j = 0; j < AT_ONCE; ++j)
-      if (i0 + j * 64 * kWaves < rows * Q4) store(blk.row0 + r[j], o[j], at[j] / 4, lse_of[r[j]]);
+      if (i0 + j * THREADS < rows * Q4) store(blk.row0 + r[j], o[j], at[j] / 4, lse_of[r[j]]);
   }
 }
 
@@ -637,20 +694,48 @@ size_t attn_prefill_workspace(int D, int Hq, int Hkv, int n_seqs, int n_tokens) 
   return kAttnDataOff + (size_t)part_rows_of(Hq, Hkv, n_tokens) * Hkv * (D + 4) * sizeof(float);
 }
 
-hipError_t launch_attn_prefill(const AttnDesc &d, void *ws, hipStream_t s) {
+namespace {
+
+template <int DT, int D, int GROUPS>
+hipError_t launch(const AttnDesc &d, void *ws, hipStream_t s) {
   // Every block of whole rows, and the items that cutting some may add: up to
   // a full round of workgroups, or a round more where sequences may differ in
   // length; none from four rounds on, whose end is short anyway.
   const int64_t blocks = (int64_t)d.n_tokens * d.G / kRows + d.n_seqs;
-  const int slots = std::max(kSlots / d.Hkv, 1), part_rows = part_rows_of(d.Hq, d.Hkv, d.n_tokens);
+  const int slots = std::max(kSlots / GROUPS / d.Hkv, 1), part_rows = part_rows_of(d.Hq, d.Hkv, d.n_tokens);
   const int extra = blocks < slots ? slots - (int)blocks : blocks < 4 * slots && d.n_seqs > 1 ? slots : 0;
   const int64_t items = blocks + extra;
-  auto *k = d.D == 64 ? (d.dtype == DT_F16 ? attn_prefill_kernel<DT_F16, 64> : attn_prefill_kernel<DT_BF16, 64>)
-                      : (d.dtype == DT_F16 ? attn_prefill_kernel<DT_F16, 128> : attn_prefill_kernel<DT_BF16, 128>);
-  hipLaunchKernelGGL(k, dim3((unsigned)(items * d.Hkv)), dim3(64 * kWaves), 0, s, d, part_rows, extra > 0 ? (int)items : 0,
-                     (uint32_t *)ws, (float *)((char *)ws + kAttnDataOff),
-                     (int)((size_t)part_rows * d.Hkv * (d.D + 4) * sizeof(float)));
+  hipLaunchKernelGGL((attn_prefill_kernel<DT, D, GROUPS>), dim3((unsigned)(items * d.Hkv)),
+                     dim3(64 * kWaves * GROUPS), 0, s, d, part_rows, extra > 0 ? (int)items : 0, (uint32_t *)ws,
+                     (float *)((char *)ws + kAttnDataOff),
+                     (int)((size_t)part_rows * d.Hkv * (D + 4) * sizeof(float)));
   return hipGetLastError();
+}
+
+// Two groups of waves a workgroup where one workgroup a CU takes all whole
+// blocks: what bounds such a call is a block's chain of tiles, which two groups
+// halve without partial sums in memory (1024 tokens of 32 / 8 heads over 1024
+// keys 49 -> 27 us, over 4096 100 -> 81; 256 of 32 heads over 4096 73 -> 51).
+// One group with more blocks, where two of them on a CU hide each other's waits
+// (2048 tokens of 32 heads over 2048 keys 59 us, with two groups 70), with
+// blocks that are half empty (4 x 33..64 tokens of 32 heads, D = 64, over 4096
+// keys 34 and 37) and on short tables (16 tokens 7.4 and 8.2).
+template <int DT, int D>
+hipError_t launch(const AttnDesc &d, void *ws, hipStream_t s) {
+  const int64_t rows = (int64_t)d.n_tokens * d.G, blocks = (rows + (int64_t)(kRows - 1) * d.n_seqs) / kRows;
+  const int64_t room = (int64_t)d.width * d.page_size;
+  const int64_t keys = d.window > 0 ? std::min<int64_t>(room, (int64_t)d.window + d.sinks) : room;
+  return 2 * rows > (int64_t)kRows * d.n_seqs && blocks * d.Hkv <= kSlots / 2 && keys >= 8 * kKeys
+             ? launch<DT, D, 2>(d, ws, s)
+             : launch<DT, D, 1>(d, ws, s);
+}
+
+}  // namespace
+
+hipError_t launch_attn_prefill(const AttnDesc &d, void *ws, hipStream_t s) {
+  if (d.D == 64)
+    return d.dtype == DT_F16 ? launch<DT_F16, 64>(d, ws, s) : launch<DT_BF16, 64>(d, ws, s);
+  return d.dtype == DT_F16 ? launch<DT_F16, 128>(d, ws, s) : launch<DT_BF16, 128>(d, ws, s);
 }
 
 }  // namespace spear

@@ -348,3 +348,41 @@ def test_refusals_on_the_gpu():
         run(c, window=-1)
     with pytest.raises(spear.SpearError, match="scale"):
         run(c, scale=float("inf"))
+
+
+# Chunks of whole blocks of rows that do not fill the chip: the tiles of a block are shared out
+# inside a workgroup and, with more of them, among workgroups; odd and even numbers of tiles.
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 5), (1100, 0)])
+@pytest.mark.parametrize("lens,chunks", [([577], [140]), ([2111], [200]), ([1800, 640, 1300], [257, 128, 99]),
+                                         ([4001], [128]), ([1500, 900], [130, 900])])
+@pytest.mark.parametrize("heads,dim,dtype", [((2, 2), 128, "bf16"), ((4, 1), 64, "f16")])
+def test_chunks_of_few_blocks_over_long_caches(heads, dim, dtype, lens, chunks, window, sinks):
+    c = make_case(sum(lens), lens, heads, dim, 16, dtype, chunks)
+    verify(c, f"chunk lens={lens} chunks={chunks} window={window} {dtype}", window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+@pytest.mark.parametrize("length", [700, 1237, 1300, 2113])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_hidden_positions_of_few_blocks_over_long_caches(fill, length, dim):
+    """What only the window's first tiles and the chunk's last ones hold, as above."""
+    n = 150
+    past = length - n
+    for window, bad in [(0, [length - 1, length - 20, past + 100]), (513, [past - 512, past - 470, length - 2])]:
+        c = make_case(length, [length], (2, 2), dim, 16, "bf16", [n])
+        scale = 1 / math.sqrt(dim)
+        clean = reference(c, scale, window, 0)
+        for j in bad:
+            for t in (c.k, c.v):
+                t[c.table[0, j // 16], :, j % 16] = fill
+        note(f"hidden positions hold {fill}: length={length} window={window} dim={dim}")
+        out, lse = run(c, window=window)
+        torch.cuda.synchronize()
+        sees = [r for r in range(n)
+                if any(j <= past + r and (not window or past + r - j < window) for j in bad)]
+        rows = [r for r in range(n) if r not in sees]
+        assert len(rows) >= 50 and len(sees) >= 10
+        part = Case(c.q[rows], c.k, c.v, c.table, c.lens, None, c.dtype)
+        check(out[rows], lse[rows], [a[rows] for a in clean], part, scale, "rows that see only numbers")
+        if math.isnan(fill):
+            assert torch.isnan(out[sees]).any(-1).all()
