@@ -715,7 +715,8 @@ hipError_t launch(const AttnDesc &d, void *ws, hipStream_t s) {
 // Two groups of waves a workgroup where one workgroup a CU takes all whole
 // blocks: what bounds such a call is a block's chain of tiles, which two groups
 // halve without partial sums in memory (1024 tokens of 32 / 8 heads over 1024
-// keys 49 -> 27 us, over 4096 100 -> 81; 256 of 32 heads over 4096 73 -> 51).
+// keys 49 -> 27 us, 32 with one group and no block cut; over 4096 100 -> 81;
+// 256 of 32 heads over 4096 73 -> 51).
 // One group with more blocks, where two of them on a CU hide each other's waits
 // (2048 tokens of 32 heads over 2048 keys 59 us, with two groups 70), with
 // blocks that are half empty (4 x 33..64 tokens of 32 heads, D = 64, over 4096
