@@ -76,7 +76,8 @@ __device__ __forceinline__ int v_swizzle(int t) {
 struct Tiles {  // (p_min <= p_max)
   int sink_tiles, lo_tile, count;
   __device__ __forceinline__ Tiles(const AttnDesc &d, int p_min, int p_max) {
-    const int lo = d.window > 0 ? max(0, p_min - d.window + 1) : 0;
+    // (p_min may be negative and the window as large as the type holds)
+    const int lo = d.window > 0 && p_min >= d.window ? p_min - d.window + 1 : 0;
     lo_tile = lo / kKeys;
     sink_tiles = min((min(d.sinks, lo) + kKeys - 1) / kKeys, lo_tile);
     count = p_max < 0 ? 0 : sink_tiles + p_max / kKeys + 1 - lo_tile;
