@@ -55,6 +55,7 @@ constexpr int kRows = 128;  // query rows of a workgroup
 constexpr int kKeys = 64;   // keys of a tile
 constexpr int kWaves = 4;   // of 32 rows each
 constexpr float kSlack = 8.f;  // by how much a maximum may pass m
+constexpr float kFar = 1048576.f;  // of m from 0: past this m is subtracted from the scores by itself
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
@@ -281,8 +282,7 @@ __global__ __launch_bounds__(64 * kWaves * GROUPS, 2) void attn_prefill_kernel(
       if (d.scale < 0.f) q[k] ^= 0x80008000u;
     }
   }
-  // scores stay unscaled (a negative scale has turned the query's sign): the
-  // weight is 2^(s scale - m scale), one fma
+  // scores stay unscaled (a negative scale has turned the query's sign)
   const float scale = fmaxf(fabsf(d.scale) * kLog2e, 1e-30f), slack = kSlack / scale;
 
   // Staging this wave's 16 keys of a tile: load j brings the RPI rows from
@@ -457,7 +457,6 @@ __global__ __launch_bounds__(64 * kWaves * GROUPS, 2) void attn_prefill_kernel(
 #pragma unroll
           for (int v = 0; v < 16; ++v) acc[b][v] *= f;
       }
-      const float shift = -m * scale;
       if (dirty) {
         // Values that are not finite: how many of a sign (of both, for no
         // number) a row sees of each dim, as products of ones; then they leave
@@ -500,6 +499,18 @@ __global__ __launch_bounds__(64 * kWaves * GROUPS, 2) void attn_prefill_kernel(
         }
         lds_barrier();
         if (!mine) return;
+      }
+      // The weight is 2^(s scale - m scale), one fma: m scale is rounded first, which
+      // puts every weight of the row off by one factor (sums and lse with them), of
+      // 2^(1/32) at most up to 2^20.  Further out the factor would pass what the types
+      // span: there m is subtracted first.
+      float shift = -m * scale;
+      if (__any(fabsf(shift) > kFar)) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) s[u][v] -= m;
+        shift = 0.f;
       }
       // The two products in steps of one MFMA, the next fragments' reads and a
       // share of the weights' arithmetic, which keeps both units busy; the

@@ -46,3 +46,51 @@ def test_windows_and_sinks_at_the_types_limit(lens, chunks, heads, window, sinks
     c = make_case(3, lens, heads, 64, 16, "f16", chunks)
     out, lse = run(c, window, sinks)
     check(out, lse, reference(c, 1 / 8, window, sinks), c, 1 / 8, "window at the limit")
+
+
+# ---------------------------------------------------------------------- the size of scores
+
+def equal_scores(dtype, shape, a, b, heads=(4, 2)):
+    """A case of shape `shape` whose keys score a b exactly or, two of three, 3/4 |a b| less."""
+    lens, chunks = shape
+    c = make_case(7, lens, heads, 64, 16, dtype, chunks)
+    c.q.zero_(), c.k.zero_()
+    c.q[..., 0] = a
+    top = torch.arange(c.k.shape[2]) % 3 == 0
+    c.k[..., 0] = torch.where(top, b, b - abs(0.75 * b)).to(c.k.dtype)
+    return c
+
+
+def check_equal_scores(c, scale, a, b):
+    """Where differences of scores are hundreds or more a row is the mean of the values of the keys
+    with the largest one, whose scores are one exact product: weights are 1 or 0, each rounding of
+    them is one of h, of the result another; the sums add 2^-20 and count 2^-24."""
+    out, lse = run(c, scale=scale)
+    a, b = (float(torch.tensor(x, dtype=c.k.dtype)) for x in (a, b))
+    h = torch.finfo(c.k.dtype).eps / 2
+    S, G, got, z, values = c.k.shape[2], c.q.shape[1] // c.k.shape[1], f64(out), f64(lse), f64(c.v)
+    starts = list(range(len(c.lens) + 1)) if c.starts is None else c.starts
+    for s, length in enumerate(c.lens):
+        n = starts[s + 1] - starts[s]
+        for i in range(n):
+            j = np.arange(length - n + i + 1)
+            j = j[(j % S) % 3 == 0]
+            v = values[c.table[s, j // S], :, j % S]
+            for head in range(c.q.shape[1]):
+                vv = v[:, head // G]
+                tol = (2 * h + 2.0 ** -20 + len(j) * 2.0 ** -24) * np.abs(vv).mean(0) + 2.0 ** -25
+                err = np.abs(got[starts[s] + i, head] - vv.mean(0))
+                assert (err <= tol).all(), (s, i, head, err.max())
+                want = scale * a * b + math.log(len(j))
+                assert abs(z[starts[s] + i, head] - want) <= 2.0 ** -21 * abs(want)
+
+
+@pytest.mark.parametrize("dtype,scale,a,b", [
+    ("f16", 0.125, 6e4, 6e4), ("f16", 1.0, 2e4, 2.4e4), ("f16", 1.0, 3e4, 5e4), ("f16", 1.0, 4.5e4, -3.3e4), ("f16", 1e4, 700, 900),
+    ("bf16", 1.0, 6e4, 6e4), ("bf16", -1.0, -4.5e4, -3.3e4), ("bf16", 0.125, 6e9, 4e9), ("bf16", 0.125, 2e9, -7e8)])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_scores_far_from_zero(shape, dtype, scale, a, b):
+    """Scores so large that their product with the scale is off by more than the exponents of the
+    types span."""
+    note(f"scores {scale} * {a} * {b} {dtype} {shape}")
+    check_equal_scores(equal_scores(dtype, shape, a, b), scale, a, b)
