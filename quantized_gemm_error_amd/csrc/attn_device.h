@@ -32,10 +32,10 @@ __device__ __forceinline__ int cached_len(const AttnDesc &d, int b) {
 }
 
 // Scores are kept times log2(e), so that the softmax is in powers of two; a
-// row's maximum starts at a finite value, below any score that counts, so
-// that a score of -infinity (a hidden key) weighs exactly 0.
+// row's maximum starts at the lowest finite number, so that any score passes it
+// and one of -infinity (a hidden key) weighs exactly 0.
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -1e30f;
+constexpr float kNoMax = -3.402823466e38f;
 
 // Every lane gets op over its own value and the values of the lanes 16 and
 // 32 places away: the four lanes that hold one column of a 16-wide MFMA.

@@ -94,3 +94,25 @@ def test_scores_far_from_zero(shape, dtype, scale, a, b):
     types span."""
     note(f"scores {scale} * {a} * {b} {dtype} {shape}")
     check_equal_scores(equal_scores(dtype, shape, a, b), scale, a, b)
+
+
+@pytest.mark.parametrize("scale,a,b", [(0.125, 2.0 ** 60, -(2.0 ** 57)), (1.0, 3e18, -1e19), (-1.0, -3e18, -3e19)])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_scores_near_the_lowest_number(shape, scale, a, b):
+    """Rows all of whose scores lie far below any that a mask stands for."""
+    note(f"scores {scale} * {a} * {b} {shape}")
+    check_equal_scores(equal_scores("bf16", shape, a, b), scale, a, b)
+
+
+@pytest.mark.parametrize("scale", [1e9, 1e30])
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_large_scales_of_small_scores(shape, window, scale):
+    """A scale that, times the reference of a row that has seen nothing yet, passes fp32: such rows
+    begin inside a tile of keys that the window or the chunk's order hides."""
+    note(f"scale {scale} window={window} {shape}")
+    c = make_case(7, *([shape[0], (4, 2), 64, 16, "bf16", shape[1]]))
+    c.q.div_(scale ** 0.5), c.k.div_(scale ** 0.5)
+    out, lse = run(c, window, 0, scale)
+    scale = float(np.float32(scale))
+    check(out, lse, reference(c, scale, window, 0), c, scale, "large scale")
