@@ -116,3 +116,20 @@ def test_large_scales_of_small_scores(shape, window, scale):
     out, lse = run(c, window, 0, scale)
     scale = float(np.float32(scale))
     check(out, lse, reference(c, scale, window, 0), c, scale, "large scale")
+
+
+# ----------------------------------------------------------------------------- small scales
+
+@pytest.mark.parametrize("scale", [0.0, 1e-31, -1e-38, 1e-12])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_scales_at_and_near_zero(shape, dtype, scale):
+    """Every seen value weighs the same: their mean, and the logarithm of their number."""
+    note(f"scale {scale} {dtype} {shape}")
+    c = make_case(9, shape[0], (4, 2), 64, 16, dtype, shape[1])
+    for window, sinks in ((0, 0), (100, 3)):
+        out, lse = run(c, window, sinks, scale)
+        ref = reference(c, scale, window, sinks)
+        count = ref[-1]
+        assert np.allclose(ref[1], np.where(count > 0, np.log(np.maximum(count, 1)), -np.inf)[:, None], atol=1e-9)
+        check(out, lse, ref, c, scale, f"scale {scale} window={window}")
