@@ -13,7 +13,10 @@
  *
  * Element types: queries, keys, values, cache and output share SPEAR_F16 or
  * SPEAR_BF16.  Scores, the running maximum and sum of the softmax and the
- * output sums are fp32.
+ * output sums are fp32.  The softmax's weights are rounded to the element type
+ * once, each relative to its own size, before they meet the values (their sum
+ * takes them unrounded); a SPEAR_F16 weight below 2^-27 of its row's largest is
+ * off by up to 2^-38 of that instead.
  */
 #ifndef SPEAR_ATTN_H
 #define SPEAR_ATTN_H

@@ -1,8 +1,8 @@
 // Attention of one new token per sequence over the paged cache.
 //
 // With s_j = q . k_j log2(e) scale over the visible keys j, every wave keeps
-// a running maximum m, l = sum 2^(s_j - m) and o = sum 2^(s_j - m) v_j over
-// its share of the keys; parts join as
+// a reference m, its maximum so far less kLift, l = sum 2^(s_j - m) and
+// o = sum 2^(s_j - m) v_j over its share of the keys; parts join as
 //     M = max m_i,  L = sum 2^(m_i - M) l_i,  o = sum 2^(m_i - M) o_i / L.
 //
 // Each key and value is read once, so the floor is the cache's bytes over the
@@ -279,8 +279,12 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) void attn_decode_kernel(A
       float top = x[0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-      if (__any(top > m)) {
-        const float m2 = fmaxf(m, columns_max(top)), f = __builtin_amdgcn_exp2f(m - m2);
+      if (__any(top - m > kLift<DT>)) {
+        const float most = columns_max(top);
+        float m2 = most - kLift<DT>;
+        if (!(most - m2 <= kLift<DT>)) m2 = most;  // (rounded further down, or an infinity)
+        m2 = fmaxf(m, m2);
+        const float f = __builtin_amdgcn_exp2f(m - m2);
         m = m2;
         l *= f;
 #pragma unroll

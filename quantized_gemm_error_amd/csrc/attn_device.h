@@ -37,6 +37,15 @@ __device__ __forceinline__ int cached_len(const AttnDesc &d, int b) {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.402823466e38f;
 
+// Weights are rounded to the type for the second product.  In fp16 a row's weights
+// lie around 2^kLift: around 1 its tail would be lost to what fp16 holds below 2^-14
+// (of 32767 keys 17.5 below one in the exponent of e, 2^-25.2 each, nothing would
+// reach the output, while l has them).  So a weight keeps fp16's precision down to
+// 2^-27 of the row's largest and is at most 2^-38 of it off below.  bf16 has fp32's
+// range.
+template <int DT>
+constexpr float kLift = DT == DT_F16 ? 13.f : 0.f;
+
 // Every lane gets op over its own value and the values of the lanes 16 and
 // 32 places away: the four lanes that hold one column of a 16-wide MFMA.
 // (permlane swaps of a register with itself put both halves side by side.)

@@ -1,10 +1,10 @@
 // Causal attention of the batch's new tokens over the paged cache.
 //
 // With s = q . k scale log2(e), tiles of 64 keys pass by a block of query rows
-// that keeps a reference m >= (row maximum) - 8, l = sum 2^(s - m) and
-// o = sum 2^(s - m) v in fp32 (m is raised, and l and o scaled, only when a
-// maximum passes it by more than 8: the weights stay below 2^8, and their
-// relative rounding is the same); out = o / l, lse = ln 2 (m + log2 l).
+// that keeps a reference m >= (row maximum) - kSlack, l = sum 2^(s - m + kLift) and
+// o = sum 2^(s - m + kLift) v in fp32 (m is raised, and l and o scaled, only when a
+// maximum passes it by more than kSlack: the weights stay in the type's range, and
+// their relative rounding is the same); out = o / l, lse = ln 2 (m + log2 l - kLift).
 //
 // The work is two matrix products, 4 D flops per visible pair, so MFMA bounds
 // it.  A group of four waves owns 128 rows of one key-value head (a workgroup is
@@ -54,8 +54,12 @@ namespace {
 constexpr int kRows = 128;  // query rows of a workgroup
 constexpr int kKeys = 64;   // keys of a tile
 constexpr int kWaves = 4;   // of 32 rows each
-constexpr float kSlack = 8.f;  // by how much a maximum may pass m
-constexpr float kFar = 1048576.f;  // of m from 0: past this m is subtracted from the scores by itself
+// By how much a maximum may pass m: with kLift and the shift's rounding (2^-9) less
+// than 2^16, where fp16 ends.  (fp16 with 1 instead 2% slower, with 4 1% faster: m is
+// raised and the sums scaled in more or fewer tiles.)
+template <int DT>
+constexpr float kSlack = DT == DT_F16 ? 2.9f : 8.f;
+constexpr float kFar = 65536.f;  // of m from 0: past this m is subtracted from the scores by itself
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
@@ -285,7 +289,7 @@ __global__ __launch_bounds__(64 * kWaves * GROUPS, 2) void attn_prefill_kernel(
   // scores stay unscaled (a negative scale has turned the query's sign); at a
   // scale of 0 (taken as the least normal number, so that a hidden key's weight is
   // 0 there too) the slack is infinite and m stays kNoMax
-  const float scale = fmaxf(fabsf(d.scale) * kLog2e, 1.2e-38f), slack = kSlack / scale;
+  const float scale = fmaxf(fabsf(d.scale) * kLog2e, 1.2e-38f), slack = kSlack<DT> / scale;
 
   // Staging this wave's 16 keys of a tile: load j brings the RPI rows from
   // j RPI on, this lane the chunk that belongs where its bytes land.  The
@@ -449,7 +453,7 @@ __global__ __launch_bounds__(64 * kWaves * GROUPS, 2) void attn_prefill_kernel(
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int v = 0; v < 16; ++v) top = fmaxf(top, s[u][v]);
-      if (looks && __any(top > m + slack)) {
+      if (looks && __any(top - m > slack)) {
         top = over_halves(top, [](float a, float b) { return fmaxf(a, b); });
         const float m2 = fmaxf(m, top), f = __builtin_amdgcn_exp2f((m - m2) * scale);
         m = m2;
@@ -503,16 +507,16 @@ __global__ __launch_bounds__(64 * kWaves * GROUPS, 2) void attn_prefill_kernel(
         if (!mine) return;
       }
       // The weight is 2^(s scale - m scale), one fma: m scale is rounded first, which
-      // puts every weight of the row off by one factor (sums and lse with them), of
-      // 2^(1/32) at most up to 2^20.  Further out the factor would pass what the types
+      // puts every weight of the row off by one factor (sums and lse with them), of at
+      // most 2^(2^-9) up to kFar.  Further out the factor would pass what the types
       // span: there m is subtracted first.
-      float shift = -m * scale;
+      float shift = kLift<DT> - m * scale;
       if (__any(fabsf(shift) > kFar)) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int v = 0; v < 16; ++v) s[u][v] -= m;
-        shift = 0.f;
+        shift = kLift<DT>;
       }
       // The two products in steps of one MFMA, the next fragments' reads and a
       // share of the weights' arithmetic, which keeps both units busy; the
@@ -607,7 +611,7 @@ __global__ __launch_bounds__(64 * kWaves * GROUPS, 2) void attn_prefill_kernel(
   if (blk.parts == 1) {
     if (!is_row) return;
     const float inv = l != 0.f ? 1.f / l : 0.f;
-    const float lse = l != 0.f ? (m * scale + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    const float lse = l != 0.f ? (m * scale + (__builtin_amdgcn_logf(l) - kLift<DT>)) * kLn2 : -INFINITY;
 #pragma unroll
     for (int b = 0; b < DB; ++b)
 #pragma unroll
@@ -662,7 +666,7 @@ __global__ __launch_bounds__(64 * kWaves * GROUPS, 2) void attn_prefill_kernel(
     const float inv = L != 0.f ? 1.f / L : 0.f;
     for (int k = 0; k < blk.parts; ++k)
       w_of[k * kRows + r] = inv * __builtin_amdgcn_exp2f((w_of[k * kRows + r] - M) * scale);
-    lse_of[r] = L != 0.f ? (M * scale + __builtin_amdgcn_logf(L)) * kLn2 : -INFINITY;
+    lse_of[r] = L != 0.f ? (M * scale + (__builtin_amdgcn_logf(L) - kLift<DT>)) * kLn2 : -INFINITY;
   }
   lds_barrier();
   constexpr int AT_ONCE = 4, Q4 = D / 4;

@@ -48,6 +48,40 @@ def test_windows_and_sinks_at_the_types_limit(lens, chunks, heads, window, sinks
     check(out, lse, reference(c, 1 / 8, window, sinks), c, 1 / 8, "window at the limit")
 
 
+# --------------------------------------------------------------------- the softmax's tail
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,chunks", [([500], None), ([4097], None), ([700], [100]), ([4097], [3]), ([32768], [1]),
+                                         ([32768], [130])])
+@pytest.mark.parametrize("depth", [8.0, 12.0, 16.0, 17.5, 19.0])
+def test_many_keys_far_below_one_with_the_value_zero(depth, lens, chunks, dtype):
+    """The first key has the weight 1 and the value 0, every other one e^-depth and 1: the result
+    is their number times that weight, not what is left of it in the type's subnormal numbers.
+
+    A weight is rounded to the type relative to its own size (h), or where it falls below fp16's
+    normal range by at most 2^-25, 2^-38 against the row's largest."""
+    note(f"tail depth={depth} lens={lens} chunks={chunks} {dtype}")
+    c = make_case(1, lens, (2, 1), 64, 16, dtype, chunks)
+    n = 1 if chunks is None else chunks[0]
+    c.q.zero_(), c.k.zero_(), c.v.fill_(1)
+    c.q[..., 0] = depth
+    c.k[c.table[0, 0], :, 0, 0] = 1
+    c.v[c.table[0, 0], :, 0] = 0
+    out, lse = run(c, scale=1.0)
+    h = torch.finfo(DTYPES[dtype]).eps / 2
+    tiny = 2.0 ** -25 if dtype == "f16" else 0.0
+    seen = lens[0] - n + 1 + np.arange(n)[:, None]
+    w = math.exp(-depth)
+    want = np.broadcast_to((seen - 1) * w / (1 + (seen - 1) * w), (n, 2))
+    # scores are exact, their exponent's factor log2 e and the exponential are good to 2^-20
+    rel = 2 * h + 2.0 ** -19 + seen * 2.0 ** -24
+    tol = rel * want + tiny * (2.0 ** -13 * (seen - 1) / (1 + (seen - 1) * w) + 1)
+    err = np.abs(f64(out) - want[..., None])
+    assert (err <= tol[..., None]).all(), (float(f64(out)[-1, 0, 0]), float(want[-1, 0]))
+    z = depth + np.log1p((seen - 1) * w)
+    assert (np.abs(f64(lse) - z) <= 2.0 ** -18 + 2.0 ** -21 * z).all()
+
+
 # ---------------------------------------------------------------------- the size of scores
 
 def equal_scores(dtype, shape, a, b, heads=(4, 2)):
