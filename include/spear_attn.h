@@ -61,7 +61,9 @@ typedef struct spear_kv_cache {
  *   q_starts     [n_seqs + 1], ascending from 0: sequence b's new tokens are
  *                rows q_starts[b] .. q_starts[b+1]-1 of q (of the new keys
  *                and values), its last positions in order.  NULL: one row
- *                per sequence.  Sequences without new tokens are fine.
+ *                per sequence.  Sequences without new tokens are fine.  Taken
+ *                as 0 when negative and as n_tokens when larger than that, by
+ *                the attention and by append.
  *   n_tokens     rows of q (n_seqs when q_starts is NULL).  Rows that no
  *                sequence covers are left as they are.
  * n_seqs <= SPEAR_ATTN_MAX_SEQS, n_tokens <= 2^24 (times n_q_heads: 2^30),

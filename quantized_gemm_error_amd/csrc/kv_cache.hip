@@ -40,7 +40,8 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendDesc d) {
       if (d.q_starts[mid] <= t) lo = mid; else hi = mid;
     }
     b = lo;
-    const int end = d.q_starts[b + 1];
+    // (within the call's rows, as the attention has it)
+    const int end = min(d.q_starts[b + 1], d.n_tokens);
     if (t < d.q_starts[b] || t >= end) return;
     pos = max(0, min(d.kv_lens[b], d.width * d.page_size)) - (end - t);
   } else {

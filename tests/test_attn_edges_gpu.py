@@ -167,3 +167,28 @@ def test_scales_at_and_near_zero(shape, dtype, scale):
         count = ref[-1]
         assert np.allclose(ref[1], np.where(count > 0, np.log(np.maximum(count, 1)), -np.inf)[:, None], atol=1e-9)
         check(out, lse, ref, c, scale, f"scale {scale} window={window}")
+
+
+# ---------------------------------------------------------------------- q_starts past the rows
+
+@pytest.mark.parametrize("starts", [[0, 8, 30], [-4, 8, 20], [0, 8, 2 ** 31 - 1], [-(2 ** 31), 8, 2 ** 31 - 1], [0, 25, 40]])
+def test_append_and_chunks_agree_on_rows_where_q_starts_leave_them(starts):
+    """q_starts count as 0 below it and as the number of rows above it, for both calls: keys and
+    values land where the queries of the same rows look for them."""
+    note(f"append and chunk, q_starts={starts}")
+    T, lens = 20, [25, 60]
+    c = make_case(5, lens, (4, 2), 64, 16, "f16", [8, 12])
+    gen = torch.Generator().manual_seed(3)
+    new = [torch.randn((T, 2, 64), generator=gen).half() for _ in range(2)]
+    k, v = c.k.cuda(), c.v.cuda()
+    cache = attn.SpearKVCache(k, v)
+    batch = attn.SpearKVBatch(on_gpu(c.table), on_gpu(lens), on_gpu(starts))
+    bounded = [min(max(s, 0), T) for s in starts]
+    attn.spear_kv_append(cache, batch, new[0].cuda(), new[1].cuda())
+    want = [torch.from_numpy(attn_ref.append_ref(old.numpy(), x.numpy(), c.table, lens, bounded))
+            for old, x in ((c.k, new[0]), (c.v, new[1]))]
+    assert torch.equal(k.cpu(), want[0]) and torch.equal(v.cpu(), want[1])
+    ws = attn.new_attn_workspace(cache, 4, 2, T)
+    out, lse = attn.spear_attn_prefill(cache, batch, c.q.cuda(), workspace=ws, return_lse=True)
+    c = Case(c.q, *want, c.table, lens, bounded, "f16")
+    check(out, lse, reference(c, 1 / 8, 0, 0), c, 1 / 8, "the chunk after it")
