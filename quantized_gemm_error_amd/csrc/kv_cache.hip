@@ -24,10 +24,12 @@ __device__ __forceinline__ bool in_range(int v, int n) { return (uint32_t)v < (u
 
 // ------------------------------------------------------------------ append
 
-// One 16-byte piece per thread: piece c of head h of row t, keys and values.
+// One 16-byte piece per thread: piece c of head h of row t, keys and values.  (The
+// blocks are numbered over both extents of the grid, one of which holds fewer than
+// 2^32 threads.)
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendDesc d) {
   const int per_head = d.D / 8, per_row = per_head * d.H;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t i = (blockIdx.x + (int64_t)gridDim.x * blockIdx.y) * kThreads + threadIdx.x;
   const int t = (int)(i / per_row);
   if (t >= d.n_tokens) return;
   const int rest = (int)(i - (int64_t)t * per_row), h = rest / per_head, c = rest - h * per_head;
@@ -387,8 +389,8 @@ __global__ __launch_bounds__(kPagesPerBlock) void rank_pages_kernel(
 
 hipError_t launch_kv_append(const AppendDesc &d, hipStream_t s) {
   const int64_t pieces = (int64_t)d.n_tokens * d.H * (d.D / 8);
-  hipLaunchKernelGGL(append_kernel, dim3((unsigned)((pieces + kThreads - 1) / kThreads)),
-                     dim3(kThreads), 0, s, d);
+  const int64_t blocks = (pieces + kThreads - 1) / kThreads, x = std::min<int64_t>(blocks, 1 << 22);
+  hipLaunchKernelGGL(append_kernel, dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)), dim3(kThreads), 0, s, d);
   return hipGetLastError();
 }
 

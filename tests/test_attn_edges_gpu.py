@@ -192,3 +192,19 @@ def test_append_and_chunks_agree_on_rows_where_q_starts_leave_them(starts):
     out, lse = attn.spear_attn_prefill(cache, batch, c.q.cuda(), workspace=ws, return_lse=True)
     c = Case(c.q, *want, c.table, lens, bounded, "f16")
     check(out, lse, reference(c, 1 / 8, 0, 0), c, 1 / 8, "the chunk after it")
+
+
+def test_append_of_more_pieces_than_a_launch_has_threads():
+    """2^24 tokens of 32 heads are 2^32 pieces of 16 bytes; all but three pages' tokens are dropped."""
+    note("append of 2^24 tokens")
+    n, page = 1 << 24, 16
+    k, v = (torch.zeros((4, 32, page, 64), dtype=torch.float16, device="cuda") for _ in range(2))
+    table = torch.full((1, n // page), -1, dtype=torch.int32, device="cuda")
+    table[0, 0], table[0, n // page // 2], table[0, -1] = 2, 0, 1
+    batch = attn.SpearKVBatch(table, on_gpu([n]), on_gpu([0, n]))
+    new = torch.arange(1, 1 + 2 * 32 * 64, dtype=torch.float32, device="cuda").div(4096).half().view(2, 1, 32, 64)
+    attn.spear_kv_append(attn.SpearKVCache(k, v), batch, new[0].expand(n, 32, 64), new[1].expand(n, 32, 64))
+    for t, x in ((k, new[0, 0]), (v, new[1, 0])):
+        for p in (0, 1, 2):
+            assert torch.equal(t[p], x[:, None].expand(32, page, 64)), p
+        assert not t[3].any()
