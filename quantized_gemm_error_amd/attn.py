@@ -131,10 +131,10 @@ class _On:
     def made(self, *tensors):
         """Tensors allocated by the call (on the current stream) and written on the given one."""
         import torch
-        st = self.stream
-        if not hasattr(st, "cuda_stream"):
-            st = torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()
-        here = torch.cuda.current_stream(tensors[0].device)
+        st, device = self.stream, tensors[0].device
+        if not hasattr(st, "cuda_stream"):  # a raw handle: of the tensors' device
+            st = torch.cuda.ExternalStream(st, device=device) if st else torch.cuda.default_stream(device)
+        here = torch.cuda.current_stream(device)
         if st.cuda_stream != here.cuda_stream:
             st.wait_stream(here)  # what the memory served before ends first
             for t in tensors:

@@ -279,3 +279,41 @@ def test_layers_of_a_cache():
     assert cache.n_layers == 3 and cache.layer(1).k.data_ptr() == k[1].data_ptr()
     with pytest.raises(ValueError):
         cache.layer(1).layer(0)
+
+
+class _Stream:
+    def __init__(self, handle, log):
+        self.cuda_stream, self.log = handle, log
+
+    def wait_stream(self, other):
+        self.log.append(("wait", self.cuda_stream, other.cuda_stream))
+
+
+@pytest.mark.parametrize("given", [0, 77, "object"])
+def test_memory_made_for_a_given_stream_waits_on_the_tensors_device(monkeypatch, given):
+    """A raw handle is taken as a stream of the tensors' device, not of the current one."""
+    log, asked = [], []
+
+    def named(name, handle):
+        def make(*args, device=None):
+            asked.append((name, args, device))
+            return _Stream(args[0] if name == "external" else handle, log)
+        return make
+
+    device = torch.device("cuda", 1)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda ptr, device=None: named("external", 0)(ptr, device=device))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: named("default", 0)(device=device))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: named("current", 5)(device=device))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+
+    class Made:
+        def record_stream(self, stream):
+            log.append(("record", stream.cuda_stream))
+
+    made = Made()
+    made.device = device
+    stream = _Stream(9, log) if given == "object" else given
+    handle = 9 if given == "object" else given
+    attn._On(device, stream).made(made)
+    assert log == [("wait", handle, 5), ("record", handle)]
+    assert asked and all(d == device for _, _, d in asked), asked
