@@ -188,17 +188,22 @@ class SpearKVBatch:
             _require(q_starts.numel() == n + 1, f"q_starts has {q_starts.numel()} entries, expected {n + 1}")
         self.block_table, self.kv_lens, self.q_starts = block_table, kv_lens, q_starts
         self.n_seqs = n
-        self.c = SpearKVBatchC(n, width, n, block_table.data_ptr(), kv_lens.data_ptr(),
-                               None if q_starts is None else q_starts.data_ptr())
-        self.ref = ctypes.byref(self.c)
+        self.ref = ctypes.byref(SpearKVBatchC(n, width, n, block_table.data_ptr(), kv_lens.data_ptr(),
+                                              None if q_starts is None else q_starts.data_ptr()))
+
+    @property
+    def c(self) -> SpearKVBatchC:
+        return self.ref._obj
 
     def rows(self, n_tokens: int):
-        """The C struct for a call with this many rows (kept: a step's calls have as many)."""
-        if n_tokens != self.c.n_tokens:
-            c = SpearKVBatchC.from_buffer_copy(self.c)
+        """The C struct for a call with this many rows (kept: a step's calls have as many).
+        Structs are never written once others can see them, so threads may share a batch."""
+        ref = self.ref
+        if n_tokens != ref._obj.n_tokens:
+            c = SpearKVBatchC.from_buffer_copy(ref._obj)
             c.n_tokens = n_tokens
-            self.c, self.ref = c, ctypes.byref(c)
-        return self.ref
+            self.ref = ref = ctypes.byref(c)
+        return ref
 
 
 class SpearKVPool:

@@ -317,3 +317,27 @@ def test_memory_made_for_a_given_stream_waits_on_the_tensors_device(monkeypatch,
     attn._On(device, stream).made(made)
     assert log == [("wait", handle, 5), ("record", handle)]
     assert asked and all(d == device for _, _, d in asked), asked
+
+
+@pytest.mark.parametrize("after", ["c", "ref"])
+def test_threads_that_share_a_batch_get_their_own_row_counts(after):
+    """Another thread's call with another number of rows, between the steps of this one's."""
+    import threading
+
+    class Interrupted(attn.SpearKVBatch):
+        between = None
+
+        def __setattr__(self, name, value):
+            super().__setattr__(name, value)
+            if name == after and self.between is not None:
+                call, self.between = self.between, None
+                other = threading.Thread(target=call)
+                other.start()
+                other.join()
+
+    batch, theirs = Interrupted(_i(3, 4), _i(3), _i(4)), []
+    batch.between = lambda: theirs.append(batch.rows(50))
+    mine = batch.rows(20)
+    assert mine._obj.n_tokens == 20 and all(r._obj.n_tokens == 50 for r in theirs)
+    for n in (50, 20, 50, 7):
+        assert batch.rows(n)._obj.n_tokens == n and batch.rows(n)._obj.n_seqs == 3
