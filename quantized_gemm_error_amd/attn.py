@@ -98,6 +98,16 @@ def _int32(t, name: str, dim: int, device=None) -> None:
     raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+_INT32_MIN, _INT32_MAX = -2 ** 31, 2 ** 31 - 1
+
+
+def _fits(value: int, name: str) -> int:
+    """value, which ctypes would cut to its low 32 bits if it did not fit them."""
+    if not _INT32_MIN <= value <= _INT32_MAX:
+        raise ValueError(f"{name}={value} does not fit in 32 bits")
+    return value
+
+
 def _gpu(device) -> None:
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, got {device}")
@@ -201,7 +211,7 @@ class SpearKVBatch:
         ref = self.ref
         if n_tokens != ref._obj.n_tokens:
             c = SpearKVBatchC.from_buffer_copy(ref._obj)
-            c.n_tokens = n_tokens
+            c.n_tokens = _fits(n_tokens, "rows")
             self.ref = ref = ctypes.byref(c)
         return ref
 
@@ -219,10 +229,11 @@ class SpearKVPool:
         _require(lens.numel() == table.shape[0], f"lens has {lens.numel()} entries, table {table.shape[0]} rows")
         _require(refs.numel() > 0 and table.numel() > 0, "the pool is empty")
         n_slots, width = table.shape
+        page_size = _fits(int(page_size), "page_size")
         words = int(load_library().spear_kv_scratch_words(refs.numel(), n_slots, width))
         if words == 0:
             raise SpearError(SPEAR_ERR_INVALID_ARGUMENT, "invalid pool sizes")
-        self.refs, self.table, self.lens, self.page_size = refs, table, lens, int(page_size)
+        self.refs, self.table, self.lens, self.page_size = refs, table, lens, page_size
         self.scratch = torch.empty(words, dtype=torch.int32, device=self.device)
         self.c = SpearKVPoolC(refs.numel(), self.page_size, n_slots, width, refs.data_ptr(),
                               table.data_ptr(), lens.data_ptr(), self.scratch.data_ptr())
@@ -238,8 +249,9 @@ class SpearKVPool:
 
 
 def spear_attn_workspace_bytes(cache: SpearKVCache, n_q_heads: int, n_seqs: int, n_tokens: int) -> int:
-    return int(load_library().spear_attn_workspace_bytes(cache.ref, int(n_q_heads), int(n_seqs),
-                                                         int(n_tokens)))
+    # (sizes that do not fit the call's 32 bits as the nearest that do, which it takes as invalid)
+    sizes = (max(-1, min(int(n), _INT32_MAX)) for n in (n_q_heads, n_seqs, n_tokens))
+    return int(load_library().spear_attn_workspace_bytes(cache.ref, *sizes))
 
 
 def new_attn_workspace(cache: SpearKVCache, n_q_heads: int, n_seqs: int, n_tokens: int):
@@ -306,6 +318,7 @@ def _attention(fn, cache, batch, q, out, scale, window, sinks, workspace, return
         if not workspace.is_contiguous() or workspace.device != device:
             raise ValueError(f"workspace must be contiguous and on {device}")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _fits(window, "window"), _fits(sinks, "sinks")
     _gpu(device)
     on = _On(device, stream)
     made = []

@@ -341,3 +341,29 @@ def test_threads_that_share_a_batch_get_their_own_row_counts(after):
     assert mine._obj.n_tokens == 20 and all(r._obj.n_tokens == 50 for r in theirs)
     for n in (50, 20, 50, 7):
         assert batch.rows(n)._obj.n_tokens == n and batch.rows(n)._obj.n_seqs == 3
+
+
+@pytest.mark.parametrize("kw", [dict(window=2 ** 32 + 100), dict(window=2 ** 31), dict(sinks=2 ** 32), dict(sinks=2 ** 63),
+                                dict(window=-(2 ** 32) + 7), dict(sinks=-(2 ** 31) - 1)])
+def test_windows_and_sinks_past_the_types_range(lib, kw):
+    """Refused, not cut to their low 32 bits."""
+    cache, batch = _handles()
+    chunk = attn.SpearKVBatch(_i(3, 4), _i(3), _i(4))
+    for call, b in ((attn.spear_attn_decode, batch), (attn.spear_attn_prefill, chunk)):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            call(cache, b, _t(3, 8, 64), **kw)
+
+
+def test_page_sizes_and_counts_past_the_types_range(lib):
+    for size in (2 ** 32 + 16, 2 ** 31):
+        with pytest.raises(ValueError, match="page_size"):
+            attn.SpearKVPool(_i(10), _i(3, 4), _i(3), size)
+    cache, _ = _handles()
+    assert attn.spear_attn_workspace_bytes(cache, 8, 3, 3) > 0
+    for bad in ((2 ** 32 + 8, 3, 3), (8, 2 ** 32 + 3, 3), (8, 3, 2 ** 32 + 3)):
+        assert attn.spear_attn_workspace_bytes(cache, *bad) == 0
+    many = _t(1, 2, 64).expand(2 ** 32 + 3, 2, 64)
+    with pytest.raises(ValueError):
+        attn.spear_kv_append(cache, attn.SpearKVBatch(_i(3, 4), _i(3), _i(4)), many, many)
+    with pytest.raises(ValueError, match="rows"):
+        attn.SpearKVBatch(_i(3, 4), _i(3), _i(4)).rows(2 ** 32 + 3)
