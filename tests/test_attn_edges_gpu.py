@@ -169,6 +169,56 @@ def test_scales_at_and_near_zero(shape, dtype, scale):
         check(out, lse, ref, c, scale, f"scale {scale} window={window}")
 
 
+# ------------------------------------------------------------- values that are not finite
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("length,n,heads,window", [
+    (200, 100, (4, 4), 0), (200, 100, (8, 2), 40),          # one group of waves
+    (1300, 150, (2, 2), 0), (1300, 150, (2, 2), 513),       # two groups
+    (4001, 128, (2, 2), 0), (4001, 128, (2, 2), 2000),      # blocks cut into parts
+    (300, 1, (4, 2), 0), (2900, 1, (2, 1), 0), (2900, 1, (2, 1), 700)])
+def test_values_that_are_not_finite_stay_in_their_dims(length, n, heads, window, dim, dtype):
+    """Finite keys; single dims of single values are infinite or no number, in tiles that some rows
+    see in part (the chunk's own tokens, the window's first ones) and in ones that all see.  Rows
+    that see one have in that dim the infinity (two of both signs, or no number: no number); every
+    other dim, and the rows that do not see it, are as without."""
+    past = length - n
+    first = max(0, past - window + 1) if window else 0      # of what the first row sees
+    plants = [(length - 1, 3, INF), (past + n // 2, 4, -INF), (past + n // 3, 5, INF), (past + n // 4, 5, -INF),
+              (past + n // 5, 6, NAN), (first + 1, 33, -INF), (first + n // 2, 34, NAN), (first + n // 2, 35, INF),
+              (first + 2 * n // 3, 36, INF), (first + n // 2 + 1, 36, -INF), ((first + past) // 2, 62, INF),
+              (past - 1, 63, -INF), (1, 11, INF), (2, 12, NAN)]
+    plants = [(j, d, x) for (j, d), x in {(j, d): x for j, d, x in plants}.items()]
+    sinks = 2 if window else 0
+    c = make_case(length, [length], heads, dim, 16, dtype, None if n == 1 else [n], gain=0.7)
+    scale = 1 / math.sqrt(dim)
+    clean = reference(c, scale, window, sinks)
+    for j, d, x in plants:
+        c.v[c.table[0, j // 16], :, j % 16, d] = x
+    note(f"not finite: length={length} n={n} window={window} dim={dim} {dtype}")
+    out, lse = run(c, window, sinks)
+    got, p = f64(out), past + np.arange(n)
+    sees = [(j <= p) & ((p - j < window) | (j < sinks) if window else True) for j, _, _ in plants]
+    want = np.zeros((n, dim))                               # 0: as without
+    for rows, (_, d, x) in zip(sees, plants):
+        with np.errstate(invalid="ignore"):
+            want[rows, d] += x                              # inf - inf, as inf + NaN, is NaN
+    for h in range(heads[0]):
+        for x in (INF, -INF):
+            assert (got[:, h][want == x] == x).all(), (h, x)
+        assert np.isnan(got[:, h][np.isnan(want)]).all(), h
+    planted = np.broadcast_to((want != 0)[:, None], got.shape)
+    assert planted.any()
+    # the others against the oracle without the plants (whose own dims are left out on both sides)
+    fixed = out.clone()
+    fixed[torch.from_numpy(planted.copy()).cuda()] = torch.from_numpy(clean[0][planted]).to(out.dtype).cuda()
+    check(fixed, lse, clean, c, scale, "the other dims")
+
+
 # ---------------------------------------------------------------------- q_starts past the rows
 
 @pytest.mark.parametrize("starts", [[0, 8, 30], [-4, 8, 20], [0, 8, 2 ** 31 - 1], [-(2 ** 31), 8, 2 ** 31 - 1], [0, 25, 40]])
