@@ -3,8 +3,10 @@
 import os
 import sys
 
+import numpy as np
 import pytest
 
+from attn_helpers import Case, check, reference
 from gpu_helpers import note
 
 torch = pytest.importorskip("torch")
@@ -45,3 +47,63 @@ def test_samples_differ_and_share_the_prompt():
     t = block.pool.table
     held.index_add_(0, t[t >= 0].long(), torch.ones_like(t[t >= 0]))
     assert torch.equal(held, refs)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 4)])
+def test_outputs_are_the_same_without_compaction(window, sinks, monkeypatch):
+    """Bit for bit: compaction moves pages, and nothing that is read from them changes."""
+    note(f"serve block with and without compaction, window={window}")
+    base = serve_block.serve(serve_block.Block(window=window, sinks=sinks, **KW), compact_at=4)
+    held = []
+    monkeypatch.setattr(serve_block.attn, "spear_kv_compact", lambda pool, cache: held.append((pool.refs > 0).nonzero()))
+    spread = serve_block.serve(serve_block.Block(window=window, sinks=sinks, **KW), compact_at=4)
+    assert len(held) == 1 and int(held[0].max()) + 1 > held[0].numel()  # pages that compaction moves
+    assert len(base) == len(spread) and all(torch.equal(a, b) for a, b in zip(base, spread))
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 4)])
+def test_the_blocks_attention_against_the_oracle(window, sinks, monkeypatch):
+    """Every step's attention, chunks, forks and compaction on the way, from the keys and values
+    that the projections gave for each sequence's own tokens and its parent's."""
+    note(f"serve block against the oracle, window={window}")
+    block = serve_block.Block(window=window, sinks=sinks, **KW)
+    Hq, H, D = block.q_heads, block.kv_heads, block.head_dim
+    steps, seen = [], {}
+    step, linear, fork = block.step, block._linear, serve_block.attn.spear_kv_fork
+
+    def kept_step(x, slots, lens, rows=None):
+        n = slots.numel()
+        steps.append({"slots": slots.tolist(), "lens": lens.tolist(),
+                      "starts": list(range(n + 1)) if rows is None else rows.tolist()})
+        return step(x, slots, lens, rows)
+
+    def kept_linear(layer, x):
+        y = linear(layer, x)
+        steps[-1]["qkv" if layer is block.qkv else "o"] = (y if layer is block.qkv else x).clone()
+        return y
+
+    def kept_fork(pool, src, dst, stream=None):
+        steps.append({"fork": list(zip(src.tolist(), dst.tolist()))})
+        return fork(pool, src, dst, stream)
+
+    block.step, block._linear = kept_step, kept_linear
+    monkeypatch.setattr(serve_block.attn, "spear_kv_fork", kept_fork)
+    serve_block.serve(block, tokens=6, compact_at=3)
+    torch.cuda.synchronize()
+    assert sum("o" in s for s in steps) == 3 + 6           # three steps of chunks, six of single tokens
+    for i, s in enumerate(steps):
+        if "fork" in s:
+            seen.update({b: [t.clone() for t in seen[a]] for a, b in s["fork"]})
+            continue
+        heads = s["qkv"].cpu().unflatten(1, (-1, D))
+        n = len(s["slots"])
+        k, v = torch.zeros((2, n, H, max(s["lens"]), D), dtype=heads.dtype)
+        for b, slot in enumerate(s["slots"]):
+            new = slice(s["starts"][b], s["starts"][b + 1])
+            for j, (pages, first) in enumerate(((k, Hq), (v, Hq + H))):
+                old = seen.setdefault(slot, [heads.new_zeros((0, H, D)) for _ in range(2)])
+                old[j] = torch.cat([old[j], heads[new, first:first + H]])
+                assert len(old[j]) == s["lens"][b]
+                pages[b, :, :s["lens"][b]] = old[j].transpose(0, 1)
+        c = Case(heads[:, :Hq], k, v, np.arange(n)[:, None], s["lens"], s["starts"], "f16")
+        check(s["o"].unflatten(1, (Hq, D)), None, reference(c, D ** -0.5, window, sinks), c, D ** -0.5, f"step {i}")
