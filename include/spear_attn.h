@@ -188,8 +188,8 @@ spear_status_t spear_kv_fork(const spear_kv_pool_t *pool, const int32_t *src, co
 
 /*
  * Make slots[i] ready to hold new_lens[i] tokens, i < n <=
- * SPEAR_KV_MAX_ENTRIES, in order (distinct slots; new_lens[i] no more than
- * the present length changes nothing): where its last page is part full and
+ * SPEAR_KV_MAX_ENTRIES, in order (distinct slots, so n <= n_slots; new_lens[i]
+ * no more than the present length changes nothing): where its last page is part full and
  * other rows hold it too, the slot gets a copy of that page, made here in all
  * layers of the cache; the last holder of such a page keeps it.  Then pages
  * are added up to new_lens[i] and lens[slots[i]] = new_lens[i].

@@ -326,6 +326,9 @@ spear_status_t spear_kv_reserve(const spear_kv_pool_t *pool, const spear_kv_cach
   TRY(check_pool_cache(pool, cache));
   TRY(check_list("slots", slots, n, SPEAR_KV_MAX_ENTRIES));
   TRY(check_list("new_lens", new_lens, n, SPEAR_KV_MAX_ENTRIES));
+  // (distinct slots ask for at most n_slots * table_width <= 2^30 pages, which the plan's sums hold)
+  if (n > pool->n_slots)
+    return fail(SPEAR_ERR_INVALID_ARGUMENT, "n=%d entries of a pool of %d slots are not distinct", n, pool->n_slots);
   if (!missing || !aligned(missing, 4))
     return fail(SPEAR_ERR_INVALID_ARGUMENT, "missing must be a 4-byte aligned device pointer");
   return hip_status(launch_kv_reserve(*pool, page_desc(*cache), slots, new_lens, n, missing,

@@ -367,3 +367,10 @@ def test_page_sizes_and_counts_past_the_types_range(lib):
         attn.spear_kv_append(cache, attn.SpearKVBatch(_i(3, 4), _i(3), _i(4)), many, many)
     with pytest.raises(ValueError, match="rows"):
         attn.SpearKVBatch(_i(3, 4), _i(3), _i(4)).rows(2 ** 32 + 3)
+
+
+def test_more_entries_than_slots_are_refused(lib):
+    """They cannot be distinct, and their pages could be more than the plan's 32-bit sums hold."""
+    p, c, a, b = _pool(n_slots=4), _cache(), 1 << 36, 1 << 37
+    assert lib.spear_kv_reserve(R(p), R(c), a, b, 5, 1 << 38, None) == INVALID
+    assert "5" in spear.spear_last_error()
