@@ -713,17 +713,34 @@ def serving_step(torch, device, steps=5):
     return {"chunk": C, "decode_tokens": n_dec, "ec_blocks": sorted(ecs), "step_ms": round(t, 3)}
 
 
+def further_operator_cases(listed):
+    """Chunk calls between the listed cases: chunks that do not fill the chip, short ones over long
+    caches (a cached prefix, drafted tokens) and a merged step at head_dim 128."""
+    by = {c["name"]: c for c in listed}
+
+    def chunk(like, name, length, tokens, heads, **kw):
+        return dict(by[like], name=name, min_len=length[0], max_len=length[1], min_chunk=tokens[0],
+                    max_chunk=tokens[1], q_heads=heads[0], kv_heads=heads[1], **kw)
+
+    one = {n: chunk("chunk_late", f"chunk_1024_of_{n}", (n, n), (1024, 1024), (32, 8)) for n in (1024, 4096, 16384)}
+    return [*one.values(),
+            chunk("chunk_first", "chunk_256_of_4096", (4096, 4096), (256, 256), (32, 32)),
+            chunk("chunk_window", "chunk_two_short", (4000, 4096), (100, 128), (32, 32), window=0, sinks=0),
+            chunk("chunk_late", "chunk_16_of_16384", (16384, 16384), (16, 16), (64, 8)),
+            chunk("chunk_mixed", "chunk_mixed_128", (300, 1500), (129, 256), (32, 8), head_dim=128)]
+
+
 def operators_context(torch, calls):
-    """The cases of perf/operators.py (the paged cache and its attention) through the library:
-    each case's call on three sets of inputs in turn, `calls` of them in one captured graph; the
-    median time of a call over five replays."""
+    """The cases of perf/operators.py (the paged cache and its attention) and a few chunk calls
+    between them through the library: each case's call on three sets of inputs in turn, `calls` of
+    them in one captured graph; the median time of a call over five replays."""
     import importlib.util
     spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
     ops = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(ops)
     ops.own = True
     out = {}
-    for case in ops.listed():
+    for case in ops.listed() + further_operator_cases(ops.listed()):
         states = [ops.prepare(case, seed) for seed in (1, 2, 3)]
         for st in states:
             ops.run(st)
@@ -1211,7 +1228,8 @@ def main():
                          "stream) and print it")
     ap.add_argument("--operators", type=int, metavar="CALLS",
                     help="time only the paged cache's operators and its attention (the cases of "
-                         "perf/operators.py), CALLS calls of each in a graph, and print them")
+                         "perf/operators.py and a few chunk calls between them), CALLS calls of "
+                         "each in a graph, and print them")
     args = ap.parse_args()
     if args.summarize_profiles:
         summarize_profiles(*args.summarize_profiles, out_dir=os.path.join(ROOT, "profiles"))

@@ -31,8 +31,8 @@
 //
 // The work of a head is one list: the 32-key tiles that the sequences' queries
 // see, one sequence after the other.  It is cut into R equal runs, whatever the
-// lengths, R such that the workgroups (R runs x heads) all run at once, and
-// the heads go through it in step, which keeps the reads of one moment in the
+// lengths, R such that the workgroups (R runs x heads) fill the last of one to
+// four rounds of them (see runs_of), and the heads go through it in step, which keeps the reads of one moment in the
 // same pages (one list over heads and sequences: 212 us where this takes 190).
 // A workgroup's waves stream through their run without a pause: the next
 // tile's loads are issued before the present one's products, across the ends
@@ -127,6 +127,8 @@ struct Stretch {
   int begin, next;  // list positions of the sequence's start and end
 };
 
+// (D = 64 in 128 registers, for two workgroups a CU, keeps two addresses of 8 bytes
+// in scratch, each read once a stretch.)
 template <int DT, int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) void attn_decode_kernel(AttnDesc d, int heads, int head_blocks,
                                                               int runs, uint32_t *counters, float *parts,
@@ -429,8 +431,10 @@ int head_blocks_of(int Hq, int Hkv) { return (Hq / Hkv + 15) / 16; }
 // waves with the registers of D = 128 and two of D = 64.
 int slots_of(int D) { return D == 64 ? 512 : 256; }
 
-// Runs per head: the number, up to four rounds of workgroups, with which the
-// last round is fullest; the fewest of equals.
+// Runs per head: the number, up to four rounds of workgroups, from which on no
+// larger one fills the last round by 5% of a round more (256 workgroups at once:
+// 1 head takes 247 runs, 8 take 32, 12 take 64 in three full rounds, 33 take 15
+// in two).
 int runs_of(int D, int heads) {
   const int slots = slots_of(D);
   int best = 1;

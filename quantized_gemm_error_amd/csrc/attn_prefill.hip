@@ -34,8 +34,8 @@
 // and take a slower path if they hold any.
 //
 // Measured (MI355X, graph-replayed): 2048 rows of 64 / 8 heads over 16384 keys
-// 0.91 ms (1.13 PFLOP/s; a large bf16 matrix product of the library reaches
-// 1.21), two chunks in windows of 4096 147 us (917 TFLOP/s), a 2048-token first
+// 0.92 ms (1.12 PFLOP/s; a large bf16 matrix product of the library reaches
+// 1.21), two chunks in windows of 4096 148 us (913 TFLOP/s), a 2048-token first
 // chunk of 32 heads 55 us (621 TFLOP/s: its longest blocks set the time),
 // chunks of 129..256 tokens with 32 single rows, D = 64, 29 us.  At the first
 // the matrix units are busy for 53% of the cycles at about 1.9 GHz; no LDS
@@ -732,13 +732,19 @@ hipError_t launch(const AttnDesc &d, void *ws, hipStream_t s) {
 
 // Two groups of waves a workgroup where one workgroup a CU takes all whole
 // blocks: what bounds such a call is a block's chain of tiles, which two groups
-// halve without partial sums in memory (1024 tokens of 32 / 8 heads over 1024
-// keys 49 -> 27 us, 32 with one group and no block cut; over 4096 100 -> 81;
-// 256 of 32 heads over 4096 73 -> 51).
+// halve without partial sums in memory.  In us with two groups, one, and one with
+// no block cut: 1024 tokens of 32 / 8 heads over 1024 keys 28, 53, 30 (what is
+// gained there is that no block is cut); over 4096 78, 99, 89; over 16384 272, 278,
+// 305; 256 of 32 heads over 4096 48, 72, 82; 16 of 64 / 8 heads over 16384 57, 64,
+// 301.
 // One group with more blocks, where two of them on a CU hide each other's waits
-// (2048 tokens of 32 heads over 2048 keys 59 us, with two groups 70), with
+// (2048 tokens of 32 heads over 2048 keys 57 us, with two groups 70), with
 // blocks that are half empty (4 x 33..64 tokens of 32 heads, D = 64, over 4096
-// keys 34 and 37) and on short tables (16 tokens 7.4 and 8.2).
+// keys 35 and 39) and on short tables (16 tokens 7.3 and 8.3).
+// The rule sees what the host knows: the table's width and not the lengths in it,
+// and the rows of all sequences together.  A short cache in a wide table takes two
+// groups too, and more time for it (first chunks of 128 and 256 tokens 11.9 and
+// 13.9 us, with one group 10.4 and 12.9).
 template <int DT, int D>
 hipError_t launch(const AttnDesc &d, void *ws, hipStream_t s) {
   const int64_t rows = (int64_t)d.n_tokens * d.G, blocks = (rows + (int64_t)(kRows - 1) * d.n_seqs) / kRows;

@@ -5,7 +5,7 @@
 // sizes of one decode step, by launches: each call is one launch for the
 // bookkeeping and, where pages move, one for the bytes.  Measured (MI355X):
 // append of 32 tokens of 32 heads 3.0 us, of 5 chunks with 5672 tokens of 8
-// heads 10.4 us (4.5 TB/s); fork and reserve of 32 samples with their part-full
+// heads 10.2 us (4.6 TB/s); fork and reserve of 32 samples with their part-full
 // pages in 32 layers 28 us, of which the copies 17 us (5.8 TB/s); free and
 // compact of a 2.5 GB cache of 8 layers 231 us, the copies 217 us (5.7 TB/s).
 #include <algorithm>
