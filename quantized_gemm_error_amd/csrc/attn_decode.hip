@@ -32,12 +32,13 @@
 // The work of a head is one list: the 32-key tiles that the sequences' queries
 // see, one sequence after the other.  It is cut into R equal runs, whatever the
 // lengths, R such that the workgroups (R runs x heads) fill the last of one to
-// four rounds of them (see runs_of), and the heads go through it in step, which keeps the reads of one moment in the
-// same pages (one list over heads and sequences: 212 us where this takes 190).
-// A workgroup's waves stream through their run without a pause: the next
-// tile's loads are issued before the present one's products, across the ends
-// of sequences too.  Where a run ends inside a sequence, the parts meet in the
-// workspace and the workgroup that completes them joins them in list order.
+// four rounds of them (see runs_of), and the heads go through it in step, which
+// keeps the reads of one moment in the same pages (one list over heads and
+// sequences: 212 us where this takes 190).  A workgroup's waves stream through
+// their run without a pause: the next tile's loads are issued before the
+// present one's products, across the ends of sequences too.  Where a run ends
+// inside a sequence, the parts meet in the workspace and the workgroup that
+// completes them joins them in list order.
 //
 // Measured (MI355X, graph-replayed): 32 rows of 32 heads over 512..4144 keys
 // 190 us for 1.22 GB (6.4 TB/s; a device copy reaches 5.2), 4 rows of 64 / 8
@@ -127,8 +128,8 @@ struct Stretch {
   int begin, next;  // list positions of the sequence's start and end
 };
 
-// (D = 64 in 128 registers, for two workgroups a CU, keeps two addresses of 8 bytes
-// in scratch, each read once a stretch.)
+// (D = 64 in 128 registers, for two workgroups a CU, spills two pairs of them, each
+// read again once a stretch.)
 template <int DT, int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) void attn_decode_kernel(AttnDesc d, int heads, int head_blocks,
                                                               int runs, uint32_t *counters, float *parts,

@@ -286,10 +286,10 @@ __global__ __launch_bounds__(64 * kWaves * GROUPS, 2) void attn_prefill_kernel(
       if (d.scale < 0.f) q[k] ^= 0x80008000u;
     }
   }
-  // scores stay unscaled (a negative scale has turned the query's sign); at a
-  // scale of 0 (taken as the least normal number, so that a hidden key's weight is
-  // 0 there too) the slack is infinite and m stays kNoMax
-  const float scale = fmaxf(fabsf(d.scale) * kLog2e, 1.2e-38f), slack = kSlack<DT> / scale;
+  // scores stay unscaled (a negative scale has turned the query's sign; one of 0 is
+  // taken as 1e-37, so that a hidden key's weight is 0 there too, with a slack that
+  // any score passes from kNoMax)
+  const float scale = fmaxf(fabsf(d.scale) * kLog2e, 1e-37f), slack = kSlack<DT> / scale;
 
   // Staging this wave's 16 keys of a tile: load j brings the RPI rows from
   // j RPI on, this lane the chunk that belongs where its bytes land.  The
