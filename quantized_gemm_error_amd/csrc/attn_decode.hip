@@ -43,7 +43,7 @@
 // Measured (MI355X, graph-replayed): 32 rows of 32 heads over 512..4144 keys
 // 190 us for 1.22 GB (6.4 TB/s; a device copy reaches 5.2), 4 rows of 64 / 8
 // heads over up to 32768 keys 79 us (5.7 TB/s), 48 rows in windows of 4096 in
-// token-major pages 138 us (5.4 TB/s), one row over 257 keys 6.1 us.
+// token-major pages 139 us (5.4 TB/s), one row over 257 keys 6.2 us.
 // Tried: four-wave workgroups, three to a CU, 230 us; 128 registers at D = 128
 // for twice the waves 344 us (spills); K past the caches too 166 -> 180 us for
 // the windowed rows (its 64-byte pieces of a row come by two instructions).
