@@ -1,5 +1,6 @@
 """MI355X-native compensated 4-bit linear layer (libspear), the paged key-value cache and attention
-between such layers, and their Python binding."""
+between such layers, the norm, microscaled 4-bit products and sampling around them, and their
+Python binding."""
 
 from .spear import (  # noqa: F401
     SPEAR_BF16,
@@ -39,4 +40,21 @@ from .attn import (  # noqa: F401
     spear_kv_fork,
     spear_kv_free,
     spear_kv_reserve,
+)
+from .mx import (  # noqa: F401
+    SPEAR_F32,
+    SPEAR_MXFP4,
+    SPEAR_MXFP8,
+    SpearMX,
+    new_mx_workspace,
+    spear_mx_dequantize,
+    spear_mx_linear,
+    spear_mx_quantize,
+    spear_mx_workspace_bytes,
+    spear_rms_norm,
+)
+from .sampling import (  # noqa: F401
+    new_sample_workspace,
+    spear_sample,
+    spear_sample_workspace_bytes,
 )

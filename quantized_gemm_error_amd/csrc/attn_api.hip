@@ -1,39 +1,15 @@
 // C ABI of the paged cache and its attention (spear_attn.h): host-side
 // validation before any launch.
 #include <math.h>
-#include <stdarg.h>
-#include <stdio.h>
 
 #include <algorithm>
 
+#include "api_common.h"
 #include "attn_internal.h"
 
 using namespace spear;
 
 namespace {
-
-spear_status_t fail(spear_status_t st, const char *fmt, ...) {
-  char text[400];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(text, sizeof text, fmt, ap);
-  va_end(ap);
-  return set_last_error(st, text);
-}
-
-spear_status_t ok() { return set_last_error(SPEAR_OK, ""); }
-
-spear_status_t hip_status(hipError_t e, const char *what) {
-  if (e != hipSuccess) return fail(SPEAR_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return ok();
-}
-
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-#define TRY(expr)                                     \
-  do {                                                \
-    if (const spear_status_t st_ = (expr)) return st_; \
-  } while (0)
 
 // Whether an array of these extents and strides (elements, the innermost of
 // stride 1 first) gives every element an address of its own, with offsets

@@ -1,0 +1,434 @@
+"""Microscaled matrices, the norm and the product against the float64 oracle, through the public
+binding."""
+
+import numpy as np
+import pytest
+
+from gpu_helpers import note
+from oracle import mx_ref
+from quantized_gemm_error_amd import mx, spear
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def f32(t):
+    return t.detach().cpu().float().numpy()
+
+
+def randn(seed, shape, dtype="f16", spread=0.0):
+    """Rows of different size where spread > 0, made on the host."""
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=gen)
+    if spread:
+        x *= torch.exp(spread * torch.randn((shape[0], 1), generator=gen))
+    return x.to(DT[dtype])
+
+
+# ------------------------------------------------------------------------------------- quantizing
+
+def check_matrix(m, x, fmt, what):
+    """Codes and scales bit for bit, padding rows aside, and the values read back."""
+    codes, scales = mx_ref.quantize_ref(f64(x), fmt)
+    want_c, want_s = mx_ref.tiled_ref(codes, scales, fmt)
+    rows, cols = x.shape
+    rb, kt = -(-rows // 16), -(-cols // 128)
+    per = 16 if fmt == "fp4" else 32     # bytes of a row in a tile, in pieces of 16
+    got_c = m.codes.cpu().numpy().reshape(rb, kt, per // 16, 4, 16, 16)
+    got_s = m.scales.cpu().numpy().reshape(rb, -1, 4, 16, 4)
+    last = rows - 16 * (rb - 1)          # rows of the last block
+    keep = np.ones((rb, 16), dtype=bool)
+    keep[-1, last:] = False
+    pick = lambda a, axis: np.moveaxis(a, axis, 1)[keep]                              # noqa: E731
+    assert np.array_equal(pick(got_s, 3), pick(want_s.reshape(got_s.shape), 3)), f"{what}: scales"
+    assert np.array_equal(pick(got_c, 4), pick(want_c.reshape(got_c.shape), 4)), f"{what}: codes"
+    held = mx_ref.values_ref(codes, scales, fmt)
+    back = mx.spear_mx_dequantize(m)
+    torch.cuda.synchronize()
+    assert np.array_equal(f64(back), held.astype(np.float32).astype(np.float64), equal_nan=True), f"{what}: values"
+    for dt in ("f16", "bf16"):
+        got = mx.spear_mx_dequantize(m, DT[dt])
+        torch.cuda.synchronize()
+        assert torch.equal(torch.nan_to_num(got.cpu(), nan=7.0),
+                           torch.nan_to_num(torch.from_numpy(held).float().to(DT[dt]), nan=7.0)), f"{what}: {dt}"
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 1), (1, 31), (2, 32), (15, 33), (16, 128), (17, 129), (33, 510), (5, 512),
+                                   (40, 1000), (3, 2050)])
+def test_quantize_sizes(shape, dtype, fmt):
+    note(f"quantize {shape} {dtype} {fmt}")
+    x = randn(shape[1], shape, dtype, spread=2.0)
+    check_matrix(mx.spear_mx_quantize(x.cuda(), fmt), x, fmt, f"{shape} {dtype}")
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_quantize_every_16_bit_pattern(dtype, fmt):
+    """Each pattern in a block of its neighbours (like exponents), of random others, and alone with
+    zeros; infinities and NaN among them."""
+    note(f"quantize all patterns {dtype} {fmt}")
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    perm = torch.randperm(65536, generator=torch.Generator().manual_seed(2))
+    alone = torch.zeros((1024, 32), dtype=torch.int16)
+    alone[:, 5] = bits[::64]
+    for v in (bits.view(64, 1024), bits[perm].view(64, 1024), alone.view(32, 1024)):
+        x = v.contiguous().view(DT[dtype])
+        check_matrix(mx.spear_mx_quantize(x.cuda(), fmt), x, fmt, dtype)
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_quantize_fp32_ends(fmt):
+    """Every exponent of fp32 with values around the borders between codes, and what is not finite."""
+    note(f"quantize f32 ends {fmt}")
+    gen = torch.Generator().manual_seed(9)
+    e = torch.arange(-149, 128).repeat_interleave(2).double()[:, None]
+    table = torch.from_numpy(mx_ref.numbers(fmt))
+    mid = (table[1:] + table[:-1]) / 2
+    pick = mid[torch.randint(0, mid.numel(), (e.shape[0], 62), generator=gen)] / 2.0 ** mx_ref.TOP[fmt]
+    nudge = 1 + (torch.randint(-1, 2, pick.shape, generator=gen)) * 2.0 ** -23
+    x = torch.cat([torch.ones_like(e), pick * nudge, torch.ones_like(e)], 1) * 2.0 ** e
+    x = (x * torch.where(torch.rand(x.shape, generator=gen) < 0.5, -1.0, 1.0)).float()
+    extra = torch.zeros((4, 64))
+    extra[0, 3], extra[1, 40], extra[2, 0], extra[3, 63] = float("inf"), float("nan"), -float("inf"), -3.4e38
+    x = torch.cat([x, extra])
+    check_matrix(mx.spear_mx_quantize(x.cuda(), fmt), x, fmt, "f32")
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_quantize_strides_and_places(fmt):
+    note(f"quantize strides {fmt}")
+    big = randn(4, (40, 700), "bf16").cuda()
+    for view in (big[:, 8:520], big[1:, 3:400], big[::3, :300], big[:1].expand(20, 700), big[:0]):
+        m = mx.spear_mx_quantize(view, fmt)
+        if view.shape[0]:
+            check_matrix(m, view.cpu(), fmt, str(view.stride()))
+    # into a matrix that held others; out of range columns of an out array stay
+    m = mx.spear_mx_quantize(randn(5, (20, 700), "f32").cuda(), fmt)
+    x = randn(6, (20, 700), "f16")
+    check_matrix(mx.spear_mx_quantize(x.cuda(), out=m), x, fmt, "again")
+    wide = torch.full((20, 703), 7.0, dtype=torch.float16, device="cuda")
+    mx.spear_mx_dequantize(m, out=wide[:, 1:701])
+    torch.cuda.synchronize()
+    assert (wide[:, 0] == 7).all() and (wide[:, 701:] == 7).all()
+    assert np.array_equal(f64(wide[:, 1:701]), f64(torch.from_numpy(mx_ref.held_ref(f64(x), fmt)).half()))
+
+
+def test_quantize_far_rows():
+    """Rows that start past 2^32 bytes."""
+    note("quantize far rows")
+    big = torch.zeros(3 * (2 ** 31 + 8), dtype=torch.float16, device="cuda")
+    view = big.as_strided((3, 300), (2 ** 31 + 8, 1))
+    x = randn(8, (3, 300), "f16")
+    view.copy_(x)
+    check_matrix(mx.spear_mx_quantize(view, "fp8"), x, "fp8", "far")
+    out = torch.zeros_like(big).as_strided((3, 300), (2 ** 31 + 8, 1))
+    m = mx.spear_mx_quantize(x.cuda(), "fp8")
+    mx.spear_mx_dequantize(m, out=out)
+    torch.cuda.synchronize()
+    assert np.array_equal(f64(out), mx_ref.held_ref(f64(x), "fp8"))
+
+
+# ------------------------------------------------------------------------------------------- norm
+
+def check_norm(y, h_out, x, residual, weight, eps, dtype, what):
+    """y = (h r) w in fp32: h is rounded once (2^-24), r and both products as well, the result to
+    the type (eps / 2, or half of fp16's smallest step)."""
+    h = f64(x) if residual is None else f64(x) + f64(residual)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        ref = h / np.sqrt((h * h).mean(-1, keepdims=True) + eps) * f64(weight)
+    half = torch.finfo(DT[dtype]).eps / 2
+    tiny = 2.0 ** -25 if dtype == "f16" else 0.0
+    got = f64(y)
+    tol = np.abs(ref) * (half + 6 * 2.0 ** -24) * (1 + half) + tiny
+    assert (np.abs(got - ref) <= tol).all(), f"{what}: off by {np.max(np.abs(got - ref) / np.maximum(tol, 1e-300))} of what it may"
+    if residual is not None:
+        want = (x.float() + residual.float()).to(DT[dtype])
+        assert torch.equal(h_out.cpu(), want), f"{what}: residual"
+
+
+def exact_y(x, residual, weight, eps):
+    y, _ = mx_ref.norm_ref(f32(x), None if residual is None else f32(residual), f32(weight), eps)
+    return y
+
+
+HIDDEN = [1, 2, 7, 8, 31, 32, 33, 64, 100, 255, 512, 513, 2047, 2048, 2049, 4096, 5120, 8193, 16384]
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hidden", HIDDEN)
+def test_norm_sizes(hidden, dtype, residual):
+    for rows in (1, 3, 17):
+        note(f"norm {rows} x {hidden} {dtype} residual={residual}")
+        x = randn(hidden, (rows, hidden), dtype, spread=1.0)
+        res = randn(hidden + 1, (rows, hidden), dtype) if residual else None
+        w = randn(hidden + 2, (hidden,), dtype)
+        out = mx.spear_rms_norm(x.cuda(), w.cuda(), 1e-5, None if res is None else res.cuda())
+        torch.cuda.synchronize()
+        y, h = out if residual else (out, None)
+        check_norm(y, h, x, res, w, 1e-5, dtype, f"{rows} x {hidden}")
+        for fmt in ("fp4", "fp8"):
+            out = mx.spear_rms_norm(x.cuda(), w.cuda(), 1e-5, None if res is None else res.cuda(), out_format=fmt)
+            m, h = out if residual else (out, None)
+            torch.cuda.synchronize()
+            check_matrix(m, torch.from_numpy(exact_y(x, res, w, 1e-5)), fmt, f"{rows} x {hidden} {fmt}")
+
+
+@pytest.mark.parametrize("out_format", [None, "fp8"])
+def test_norm_largest_row_and_many_rows(out_format):
+    for rows, hidden in ((2, 65536), (2, 40001), (2100, 64), (70000, 33)):
+        note(f"norm {rows} x {hidden} {out_format}")
+        x, w = randn(rows, (rows, hidden), "bf16"), randn(3, (hidden,), "bf16")
+        y = mx.spear_rms_norm(x.cuda(), w.cuda(), out_format=out_format)
+        torch.cuda.synchronize()
+        if out_format is None:
+            check_norm(y, None, x, None, w, 1e-5, "bf16", f"{rows} x {hidden}")
+        else:
+            want = mx_ref.held_ref(exact_y(x, None, w, 1e-5).astype(np.float64), "fp8")
+            assert np.array_equal(f64(mx.spear_mx_dequantize(y)), want)
+
+
+def test_norm_in_place_and_strides():
+    note("norm in place")
+    x, res, w = randn(1, (9, 300), "f16"), randn(2, (9, 300), "f16"), randn(3, (300,), "f16").cuda()
+    a, b = x.cuda(), res.cuda()
+    y, h = mx.spear_rms_norm(a, w, 1e-6, residual=b, residual_out=b, out=a)
+    torch.cuda.synchronize()
+    assert y is a and h is b
+    check_norm(a, b, x, res, w, 1e-6, "f16", "in place")
+    a, b = x.cuda(), res.cuda()
+    y, h = mx.spear_rms_norm(a, w, 1e-6, residual=b, residual_out=a, out=b)
+    torch.cuda.synchronize()
+    check_norm(b, a, x, res, w, 1e-6, "f16", "crossed")
+    big = torch.full((9, 620), 5.0, dtype=torch.float16, device="cuda")
+    big[:, :300], big[:, 301:601] = x.cuda(), res.cuda()
+    out = torch.full((9, 303), 5.0, dtype=torch.float16, device="cuda")
+    y, h = mx.spear_rms_norm(big[:, :300], w, 1e-6, residual=big[:, 301:601], out=out[:, 2:302])
+    torch.cuda.synchronize()
+    check_norm(out[:, 2:302], h, x, res, w, 1e-6, "f16", "strided")
+    assert (out[:, :2] == 5).all() and (out[:, 302:] == 5).all()
+    y, h = mx.spear_rms_norm(x[:1].cuda().expand(9, 300), w, 1e-6, residual=res.cuda())
+    torch.cuda.synchronize()
+    check_norm(y, h, x[:1].expand(9, 300), res, w, 1e-6, "f16", "broadcast")
+
+
+def test_norm_of_zeros_and_what_is_not_finite():
+    note("norm edges")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    x[1, 5], x[2, 7] = float("inf"), float("nan")
+    x[3] = 3e38                       # its squares overflow fp32, not the sum
+    y = f64(mx.spear_rms_norm(x.cuda(), w))
+    assert (y[0] == 0).all() and np.isnan(y[1, 5]) and (np.delete(y[1], 5) == 0).all() and np.isnan(y[2]).all()
+    assert np.allclose(y[3], 1.0)
+    y = f64(mx.spear_rms_norm(x.cuda(), w, eps=0.0))
+    assert np.isnan(y[0]).all()       # 0 / 0
+    m = f64(mx.spear_mx_dequantize(mx.spear_rms_norm(x.cuda(), w, out_format="fp4")))
+    assert (m[0] == 0).all() and np.isnan(m[1, :32]).all() and (m[1, 32:] == 0).all() and np.isnan(m[2]).all()
+
+
+# ----------------------------------------------------------------------------------------- linear
+
+def check_linear(y, w, x, xf, dtype, what):
+    """Elementwise against 64 bits.  With h = eps / 2 of y's type the result is rounded once (h |y|,
+    2^-25 in fp16 at least).  Sums of fp32 lose at most 2^-23 of what they have reached each, a
+    step of 128 products and its joins count 3 of them: 3 (K / 128 + 8) 2^-23 sum |x w|.  With e4m3
+    tokens and 16-bit results the matrix unit keeps what is a 2^-16th of the largest product of a
+    step or more, so a product below that errs by itself at most, any other by that."""
+    wc, ws = mx_ref.quantize_ref(f64(w), "fp4")
+    wv = mx_ref.values_ref(wc, ws, "fp4")
+    xv = mx_ref.held_ref(f64(x), xf)
+    ref = xv @ wv.T
+    reach = np.abs(xv) @ np.abs(wv).T
+    K = x.shape[1]
+    got = f64(y)
+    assert np.array_equal(np.isfinite(got), np.isfinite(ref)), f"{what}: what is finite"
+    fine = np.isfinite(ref)
+    half = torch.finfo(y.dtype).eps / 2 if y.dtype != torch.float32 else 2.0 ** -24
+    tol = half * np.abs(ref) + (2.0 ** -25 if y.dtype == torch.float16 else 0.0) + 3 * (K / 128 + 8) * 2.0 ** -23 * reach
+    if xf == "fp8" and y.dtype != torch.float32:
+        for k in range(0, K, 128):
+            p = np.abs(xv[:, None, k:k + 128] * wv[None, :, k:k + 128])
+            p = np.nan_to_num(p)
+            tol += np.minimum(p, 2.0 ** -16 * 2 * p.max(-1, keepdims=True)).sum(-1)
+    worst = np.max((np.abs(got - ref) / np.maximum(tol, 1e-300))[fine], initial=0.0)
+    assert worst <= 1, f"{what}: {worst} of the tolerance"
+
+
+def run_linear(w, x, xf, out, ws=None, **kw):
+    wm = mx.spear_mx_quantize(w.cuda(), "fp4")
+    ws = mx.new_mx_workspace(wm, x.shape[0]) if ws is None else ws
+    return mx.spear_mx_linear(wm, x.cuda(), x_format=xf, out_dtype=DT[out], workspace=ws, **kw)
+
+
+TOKENS = [1, 2, 15, 16, 17, 31, 32, 33, 48, 63, 64, 65, 100, 128, 129, 200, 257, 300]
+
+
+@pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("xf", ["fp4", "fp8"])
+@pytest.mark.parametrize("tokens", TOKENS)
+def test_linear_tokens(tokens, xf, out):
+    note(f"linear {tokens} tokens {xf} {out}")
+    x, w = randn(tokens, (tokens, 640), "f16", spread=1.0), randn(2, (144, 640), "f16")
+    y = run_linear(w, x, xf, out)
+    torch.cuda.synchronize()
+    check_linear(y, w, x, xf, out, f"{tokens} tokens")
+
+
+@pytest.mark.parametrize("xf", ["fp4", "fp8"])
+@pytest.mark.parametrize("K", [1, 31, 32, 33, 100, 127, 128, 129, 256, 384, 500, 512, 513, 1000, 1536, 2047, 4096, 5000])
+def test_linear_columns(K, xf):
+    for tokens, out in ((1, "f32"), (5, "f16"), (40, "bf16"), (130, "f32")):
+        note(f"linear K={K} {tokens} tokens {xf} {out}")
+        x, w = randn(K, (tokens, K), "bf16"), randn(K + 1, (33, K), "bf16", spread=1.0)
+        y = run_linear(w, x, xf, out)
+        torch.cuda.synchronize()
+        check_linear(y, w, x, xf, out, f"K={K} {tokens}")
+
+
+@pytest.mark.parametrize("xf", ["fp4", "fp8"])
+@pytest.mark.parametrize("N", [1, 2, 15, 16, 17, 31, 33, 64, 127, 129, 255, 257, 1000])
+def test_linear_rows(N, xf):
+    for tokens, out in ((1, "f16"), (20, "f32"), (70, "bf16"), (260, "f16")):
+        note(f"linear N={N} {tokens} tokens {xf} {out}")
+        x, w = randn(N, (tokens, 384), "f16"), randn(N + 1, (N, 384), "f16")
+        y = run_linear(w, x, xf, out)
+        torch.cuda.synchronize()
+        check_linear(y, w, x, xf, out, f"N={N} {tokens}")
+
+
+@pytest.mark.parametrize("xf,out", [("fp8", "f16"), ("fp4", "bf16"), ("fp8", "f32"), ("fp4", "f32")])
+@pytest.mark.parametrize("tokens,N,K", [(1, 4096, 4096), (7, 2100, 11008), (24, 4096, 2048), (300, 700, 8200),
+                                        (600, 1100, 1024), (1024, 512, 640)])
+def test_linear_large(tokens, N, K, xf, out):
+    """Whole outputs at sizes that take every split, a part of them against the oracle."""
+    note(f"linear {tokens} x {N} x {K} {xf} {out}")
+    x, w = randn(N, (tokens, K), "bf16", spread=0.5), randn(K, (N, K), "bf16")
+    y = run_linear(w, x, xf, out)
+    torch.cuda.synchronize()
+    rng = np.random.default_rng(K)
+    rows = np.unique(np.r_[rng.choice(tokens, min(tokens, 12), replace=False), tokens - 1])
+    cols = np.unique(np.r_[rng.choice(N, 60, replace=False), N - 1])
+    check_linear(y[rows][:, cols], w[cols], x[rows], xf, out, "sampled")
+    # all of it against fp32 products of the same values
+    xv = mx.spear_mx_dequantize(mx.spear_mx_quantize(x.cuda(), xf))
+    wv = mx.spear_mx_dequantize(mx.spear_mx_quantize(w.cuda(), "fp4"))
+    ref = xv @ wv.t()
+    scale = (xv.abs() @ wv.abs().t())
+    off = ((y.float() - ref).abs() / (torch.finfo(DT[out]).eps * ref.abs() + 2.0 ** -12 * scale)).max()
+    assert off <= 1, float(off)
+
+
+def test_linear_takes_matrices_and_values_alike():
+    note("linear forms")
+    w = mx.spear_mx_quantize(randn(1, (200, 512), "f16").cuda(), "fp4")
+    ws = mx.new_mx_workspace(w, 70)
+    for tokens in (1, 19, 70):
+        x = randn(tokens, (tokens, 512), "f16").cuda()
+        for xf in ("fp4", "fp8"):
+            a = mx.spear_mx_linear(w, x, x_format=xf, workspace=ws)
+            b = mx.spear_mx_linear(w, mx.spear_mx_quantize(x, xf), out_dtype=torch.float16, workspace=ws)
+            big = torch.full((tokens, 900), 3.0, dtype=torch.float16, device="cuda")
+            for at in (8, 3):
+                c = mx.spear_mx_linear(w, x, y=big[:, at:at + 200], x_format=xf, workspace=ws)
+                torch.cuda.synchronize()
+                assert torch.equal(a, b) and torch.equal(a, c)
+                assert (big[:, :at] == 3).all() and (big[:, at + 200:] == 3).all()
+                big.fill_(3.0)
+    strided = randn(7, (70, 1100), "f16").cuda()
+    a = mx.spear_mx_linear(w, strided[:, 5:517], workspace=ws)
+    assert torch.equal(a, mx.spear_mx_linear(w, strided[:, 5:517].contiguous(), workspace=ws))
+    one = randn(8, (1, 512), "f16").cuda()
+    rows = mx.spear_mx_linear(w, one.expand(20, 512), workspace=ws)
+    assert (rows == rows[0]).all()
+    assert mx.spear_mx_linear(w, one[:0], workspace=ws).shape == (0, 200)
+
+
+@pytest.mark.parametrize("tokens", [1, 16, 40, 150, 300])
+@pytest.mark.parametrize("xf,out", [("fp8", "f16"), ("fp8", "f32"), ("fp4", "bf16")])
+def test_linear_what_is_not_finite_stays_in_its_row(tokens, xf, out):
+    note(f"linear not finite {tokens} {xf} {out}")
+    x, w = randn(1, (tokens, 300), "bf16"), randn(2, (50, 300), "bf16")
+    x[tokens // 2, 290], w[33, 1] = float("inf"), float("nan")
+    y = run_linear(w, x, xf, out)
+    torch.cuda.synchronize()
+    check_linear(y, w, x, xf, out, "not finite")
+    bad = torch.isnan(y.cpu())
+    assert bad[tokens // 2].all() and bad[:, 33].all() and int(bad.sum()) == 50 + tokens - 1
+
+
+def test_linear_extreme_scales():
+    """Blocks near both ends of the scale's range, whose products are ordinary numbers."""
+    note("linear extreme scales")
+    x, w = randn(1, (20, 256), "f32"), randn(2, (40, 256), "f32")
+    xs, ws = x * 2.0 ** 100, w * 2.0 ** -100
+    wm = mx.spear_mx_quantize(ws.cuda(), "fp4")
+    space = mx.new_mx_workspace(wm, 20)
+    for xf in ("fp4", "fp8"):
+        a = mx.spear_mx_linear(wm, mx.spear_mx_quantize(xs.cuda(), xf), out_dtype=torch.float32, workspace=space)
+        b = mx.spear_mx_linear(mx.spear_mx_quantize(w.cuda(), "fp4"), mx.spear_mx_quantize(x.cuda(), xf),
+                               out_dtype=torch.float32, workspace=space)
+        torch.cuda.synchronize()
+        assert torch.equal(a, b)
+
+
+def test_linear_workspace_serves_smaller_calls_with_equal_bits():
+    note("linear workspace")
+    w = mx.spear_mx_quantize(randn(3, (300, 2048), "f16").cuda(), "fp4")
+    other = mx.spear_mx_quantize(randn(4, (100, 2048), "f16").cuda(), "fp4")
+    ws = mx.new_mx_workspace(w, 300)
+    xs = {m: randn(m, (m, 2048), "f16").cuda() for m in (300, 1, 33, 128, 17)}
+    first = {m: mx.spear_mx_linear(w, x, workspace=ws) for m, x in xs.items()}
+    for m in (17, 300, 1, 128, 33, 300):
+        mx.spear_mx_linear(other, xs[m], workspace=ws)
+        assert torch.equal(mx.spear_mx_linear(w, xs[m], workspace=ws), first[m])
+    assert (ws[:mx.SPEAR_MX_HEADER_BYTES] == 0).all()
+    with pytest.raises(spear.SpearError):
+        mx.spear_mx_linear(w, xs[300], workspace=ws[:4096])
+    with pytest.raises(spear.SpearError):
+        mx.spear_mx_linear(w, xs[1])
+
+
+def test_other_streams_and_graphs():
+    note("streams and graphs")
+    x, res, wn = (randn(s, sh, "f16").cuda() for s, sh in ((1, (24, 512)), (2, (24, 512)), (3, (512,))))
+    w = mx.spear_mx_quantize(randn(4, (200, 512), "f16").cuda(), "fp4")
+    ws, ws2 = mx.new_mx_workspace(w, 24), mx.new_mx_workspace(w, 24)
+
+    def chain(space):
+        m, h = mx.spear_rms_norm(x, wn, residual=res, out_format="fp8")
+        y = mx.spear_mx_linear(w, m, out_dtype=torch.float32, workspace=space)
+        z = mx.spear_mx_linear(w, h, x_format="fp4", workspace=space)
+        return y, z, h, mx.spear_mx_dequantize(m, torch.bfloat16)
+
+    want = [t.clone() for t in chain(ws)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    m, h = mx.spear_rms_norm(x, wn, residual=res, out_format="fp8", stream=side)
+    y = mx.spear_mx_linear(w, m, out_dtype=torch.float32, workspace=ws2, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(h, want[2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(ws)
+    for i in range(4):
+        x.copy_(randn(10 + i, (24, 512), "f16"))
+        eager = [t.clone() for t in chain(ws2)]
+        torch.cuda.synchronize()
+        for t in got:
+            t.fill_(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager))
