@@ -1,33 +1,44 @@
 // Drawing tokens from logits.
 //
 // A row's tokens in descending order are its bins one after the other: bin b
-// holds the tokens with 32 (max - l) / T in [b, b + 1), so a bin is e^(1/32)
+// holds the tokens with 16 (max - l) / T in [b, b + 1), so a bin is e^(1/16)
 // wide in weight, and the tokens past the last bin weigh less than e^-64.
 // Every limit (the first k, the first whose weight passes p, the first that
-// passes u) is a place in that order: the bin comes from a prefix sum over the
-// bins' counts and weights, the place inside it from a radix descent over the
-// logits' bits, and among equal logits from the index.
+// passes u) is a place in that order.  Prefix sums over the bins' counts and
+// weights give the few bins in which those places can lie; the tokens of
+// these bins are gathered, sorted, and the places found among them.  In rows so
+// flat that they are too many, a place's bin is counted again in finer ranges.
 //
 // A token's weight is held relative to its bin's upper edge as a whole number
-// of 2^-45, so that the LDS sums do not depend on the order of the atomics.
+// of 2^-32, so that the sums do not depend on the order of the atomics; a row
+// is counted in runs of at most 2^15 tokens, so that a bin's count and weight
+// fit one 64-bit LDS atomic.
+#include <algorithm>
+
 #include "mx_device.h"
 
 namespace spear {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kBins = 2048, kBinsPerThread = kBins / kThreads;
-constexpr float kPerNat = 32.f;
-constexpr int kMassBits = 45;  // (a row's 2^18 tokens of at most 1 stay below 2^63)
+constexpr int kBins = 1024;  // one a thread
+constexpr double kPerNat = 16.0;
+constexpr int kCountShift = 48;                  // 2^15 tokens of at most 2^32 stay below it
+constexpr int kRun = 1 << 15;                    // tokens in one run
+constexpr int kList = 2048;                      // tokens that are gathered at once
+static_assert(kBins == kThreads, "a thread has one bin");
 
 struct SampleDesc {
   const void *logits;
-  int rows, vocab;
+  int rows, vocab, parts;
   int64_t stride;
   const float *u, *temperature, *top_p, *min_p;
   const int32_t *top_k;
   int32_t *tokens;
   float *logprobs;
+  uint32_t *arrived;  // [rows], 0 between calls (parts > 1)
+  uint64_t *best;     // [rows][parts]: the largest logit's key and its index, inverted
+  uint64_t *bins;     // [rows][parts][kBins]
 };
 
 // A float's bits in an order that rises with its value.
@@ -36,21 +47,66 @@ __device__ __forceinline__ uint32_t key_of(float l) {
   return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
-  return bitcast<float>(key ^ ((key >> 31) - 1u | 0x80000000u));
+  return bitcast<float>(key ^ (((key >> 31) - 1u) | 0x80000000u));
 }
 
-// A row's logits, a number for all, and where they lie in the order.
+// A row's logits in vectors of 16 bytes at their aligned places: element 0 is
+// place `skew` of vector 0; vectors first .. end - 1 lie inside the row whole.
 template <int DT>
 struct Row {
-  const typename MxType<DT>::T *p;
-  int n;
+  typedef typename MxType<DT>::T T;
+  static constexpr int kVec = 16 / sizeof(T);
+  static constexpr int kAhead = 4;  // loads in flight a thread
+  const T *p;
+  int n, skew, vecs, first, end;
   float top;     // the largest logit
-  double scale;  // 32 / T
-  __device__ __forceinline__ float at(int i) const {
-    const float l = MxType<DT>::load(p[i]);
+  double scale, width;  // 16 / T, and a bin's width in logits
+
+  __device__ Row(const SampleDesc &d, int r) {
+    p = (const T *)d.logits + (int64_t)r * d.stride;
+    n = d.vocab;
+    skew = (int)((uintptr_t)p % 16 / sizeof(T));
+    vecs = (n + skew + kVec - 1) / kVec;
+    first = skew ? 1 : 0;
+    end = (n + skew) / kVec;
+  }
+  // f(logit, index) for the logits of vectors [v0, v1), a thread's in
+  // ascending order but for those of vectors that reach over the row's ends.
+  template <typename F>
+  __device__ __forceinline__ void visit(int v0, int v1, F f) const {
+    const int a = max(v0, first), b = min(v1, end), tid = threadIdx.x;
+    for (int base = a; base < b; base += kAhead * kThreads) {
+      u32x4_t t[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (base + j * kThreads < b)
+          t[j] = *(const u32x4_t *)(p + (min(base + j * kThreads + tid, b - 1) * kVec - skew));
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int w = base + j * kThreads + tid;
+        if (w < b) {
+          T e[kVec];
+          __builtin_memcpy(e, &t[j], 16);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) f(clean(e[i]), w * kVec - skew + i);
+        }
+      }
+    }
+    // the vectors that are not whole: the first (before `first`) and the last
+    if (v0 < first && tid < kVec) {
+      const int i = tid - skew;
+      if (i >= 0 && i < n) f(clean(p[i]), i);
+    }
+    if (v1 == vecs && vecs > max(end, first) && tid < kVec) {
+      const int i = (vecs - 1) * kVec - skew + tid;
+      if (i < n) f(clean(p[i]), i);
+    }
+  }
+  static __device__ __forceinline__ float clean(T v) {
+    const float l = MxType<DT>::load(v);
     return l != l ? -__builtin_inff() : l + 0.f;  // (-0 and 0 are one logit)
   }
-  // 32 (top - l) / T; infinite where the logit is never drawn.
+  // 16 (top - l) / T; infinite where the logit is never drawn.
   __device__ __forceinline__ double depth(float l) const {
     if (l == top) return 0.0;
     if (l == -__builtin_inff() || top == __builtin_inff()) return (double)__builtin_inff();
@@ -60,324 +116,585 @@ struct Row {
 
 __device__ __forceinline__ int bin_of(double t) { return t < (double)kBins ? (int)t : kBins; }
 
-// The weight of a token in its bin, e^-(t - b) / 32, in units of 2^-45.
+// The weight of a token in its bin, e^(-f / 16) with f = t - b in [0, 1), in
+// units of 2^-32: seven terms leave less than 2^-44.
 __device__ __forceinline__ uint64_t mass_of(double t, int b) {
-  return (uint64_t)__builtin_rint(exp(((double)b - t) * (1.0 / kPerNat)) * (double)(1ull << kMassBits));
+  const double x = ((double)b - t) * (1.0 / kPerNat);
+  double e = 1.0 / 5040;
+  e = __builtin_fma(e, x, 1.0 / 720);
+  e = __builtin_fma(e, x, 1.0 / 120);
+  e = __builtin_fma(e, x, 1.0 / 24);
+  e = __builtin_fma(e, x, 1.0 / 6);
+  e = __builtin_fma(e, x, 0.5);
+  e = __builtin_fma(e, x, 1.0);
+  e = __builtin_fma(e, x, 1.0);
+  // 2^52 + e 2^32 rounds e 2^32 to a whole number in the mantissa
+  return bitcast<uint64_t>(__builtin_fma(e, 0x1p32, 0x1p52)) & 0xFFFFFFFFFFFFFull;
 }
 __device__ __forceinline__ double edge_of(int b) { return exp((double)b * (-1.0 / kPerNat)); }
-__device__ __forceinline__ double mass_value(uint64_t m, double edge) {
-  return (double)m * (1.0 / (double)(1ull << kMassBits)) * edge;
-}
+__device__ __forceinline__ double mass_value(uint64_t m, double edge) { return (double)m * 0x1p-32 * edge; }
 
 struct Shared {
-  uint32_t count[kBins];
-  uint64_t mass[kBins];
-  int count_before[kBins];     // of the bins before, then prefix sums of a descent
-  double mass_before[kBins];
-  double wave_mass[kWaves];
-  int wave_count[kWaves];
-  uint64_t best[kWaves];
-  int found;
-  int total_count;
-  double total_mass;
+  uint64_t run[kBins];        // a run's bins: count and weight in one word
+  int count[kBins], count_before[kBins];
+  double mass[kBins], mass_before[kBins], edge[kBins];
+  uint64_t list[kList];       // tokens: key << 32 | index inverted, so that they rise against the order
+  int fine_count[kBins];      // finer ranges of a bin
+  uint64_t fine_mass[kBins], fine_token[kBins];
+  uint64_t words[2][kWaves];  // what waves tell one another, every other time here and there
+  double sums[2][kWaves];
+  int listed, is_last;
 };
 
-// count_before and mass_before of the first `bins` bins, weights times
-// edge(b); every thread has n / kThreads neighbouring bins.
-template <typename Edge>
-__device__ void scan_bins(Shared &s, int bins, Edge edge) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int c[kBinsPerThread], csum = 0;
-  double m[kBinsPerThread], msum = 0.0;
-#pragma unroll
-  for (int i = 0; i < kBinsPerThread; ++i) {
-    const int b = kBinsPerThread * tid + i;
-    c[i] = b < bins ? (int)s.count[b] : 0;
-    m[i] = b < bins ? mass_value(s.mass[b], edge(b)) : 0.0;
-    csum += c[i];
-    msum += m[i];
-  }
-  int cs = csum;
-  double ms = msum;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int cu = __shfl_up(cs, o);
-    const double mu = __shfl_up(ms, o);
-    if (lane >= o) cs += cu, ms += mu;
-  }
-  if (lane == 63) s.wave_count[wave] = cs, s.wave_mass[wave] = ms;
-  __syncthreads();
-  int c0 = 0;
-  double m0 = 0.0;
-  for (int w = 0; w < wave; ++w) c0 += s.wave_count[w], m0 += s.wave_mass[w];
-  c0 += cs - csum;
-  // (the exclusive sum as the inclusive one of the thread before: monotone)
-  double before = __shfl_up(ms, 1);
-  m0 += lane ? before : 0.0;
-#pragma unroll
-  for (int i = 0; i < kBinsPerThread; ++i) {
-    const int b = kBinsPerThread * tid + i;
-    if (b < bins) s.count_before[b] = c0, s.mass_before[b] = m0;
-    c0 += c[i];
-    m0 += m[i];
-  }
-  if (tid == kThreads - 1) s.total_count = c0, s.total_mass = m0;
-  __syncthreads();
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  return bitcast<double>(lane_value(bitcast<uint64_t>(v), lane));
 }
 
-// The place of a token in the order, and the sums up to it, itself included.
+// Inclusive prefix sums over a wave in six adds with shifted operands, and
+// the value of the lane before.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double shifted(double v) {
+  const uint64_t u = bitcast<uint64_t>(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xF, false);
+  return bitcast<double>((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_scan(double v) {
+  v += shifted<0x111, 0xF>(v);  // row_shr:1
+  v += shifted<0x112, 0xF>(v);
+  v += shifted<0x114, 0xF>(v);
+  v += shifted<0x118, 0xF>(v);
+  v += shifted<0x142, 0xA>(v);  // row_bcast:15
+  v += shifted<0x143, 0xC>(v);  // row_bcast:31
+  return v;
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+__device__ __forceinline__ double lane_before(double v) { return shifted<0x138, 0xF>(v); }  // wave_shr:1
+
+// A workgroup's threads tell one another through s.words and s.sums, whose
+// halves take turns: a half is written again only after the barrier of the
+// exchange between, which every thread reaches after it has read.
+struct Turn {
+  Shared &s;
+  int half = 0;
+
+  // Sums before each thread's values, in thread order, and the totals.  (A
+  // sum before is the inclusive one of the thread before: they never fall.)
+  __device__ __forceinline__ void scan(int c, double m, int &c_before, double &m_before, int &c_all, double &m_all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int cs = wave_scan(c);
+    const double ms = wave_scan(m);
+    if (lane == 63) s.words[half][wave] = (uint64_t)cs, s.sums[half][wave] = ms;
+    __syncthreads();
+    const int ct = wave_scan(lane < kWaves ? (int)s.words[half][lane] : 0);
+    const double mt = wave_scan(lane < kWaves ? s.sums[half][lane] : 0.0);
+    c_before = cs - c + (wave ? __builtin_amdgcn_readlane(ct, uniform_wave() - 1) : 0);
+    m_before = lane_before(ms) + (wave ? lane_value(mt, uniform_wave() - 1) : 0.0);
+    c_all = __builtin_amdgcn_readlane(ct, kWaves - 1);
+    m_all = lane_value(mt, kWaves - 1);
+    half ^= 1;
+  }
+  // The first and the last thread for which `pass` holds, -1 for none.
+  __device__ __forceinline__ int first(bool pass) {
+    const uint64_t x = gather(pass), some = __ballot(x != 0);
+    if (!some) return -1;
+    const int w = __builtin_ctzll(some);
+    return 64 * w + __builtin_ctzll(lane_value(x, w));
+  }
+  __device__ __forceinline__ int last(bool pass) {
+    const uint64_t x = gather(pass), some = __ballot(x != 0);
+    if (!some) return -1;
+    const int w = 63 - __builtin_clzll(some);
+    return 64 * w + 63 - __builtin_clzll(lane_value(x, w));
+  }
+
+ private:
+  __device__ __forceinline__ uint64_t gather(bool pass) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t mine = __ballot(pass);
+    if (lane == 0) s.words[half][threadIdx.x >> 6] = mine;
+    __syncthreads();
+    const uint64_t x = lane < kWaves ? s.words[half][lane] : 0;
+    half ^= 1;
+    return x;
+  }
+  static __device__ __forceinline__ int uniform_wave() {
+    return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  }
+};
+
+// A token of the order by its number there (from 1), with the weight up to it.
 struct Place {
-  uint32_t key;
-  int index;
   int count;
   double mass, weight;
+  uint64_t token;
 };
 
 enum Want { kCount, kMassAtLeast, kMassAbove };
 
-// The smallest bin for which `pass` holds, or the last bin that is not empty.
-template <typename Pass>
-__device__ int first_bin(Shared &s, int bins, Pass pass) {
-  const int tid = threadIdx.x;
-  if (tid == 0) s.found = kBins;
-  __syncthreads();
-  int first = kBins, last = -1;
-#pragma unroll
-  for (int i = kBinsPerThread - 1; i >= 0; --i) {
-    const int b = kBinsPerThread * tid + i;
-    if (b < bins && s.count[b]) {
-      if (pass(b)) first = b;
-      last = max(last, b);
-    }
-  }
-  if (first < kBins) atomicMin(&s.found, first);
-  __syncthreads();
-  int found = s.found;
-  __syncthreads();
-  if (found < kBins) return found;
-  if (tid == 0) s.found = -1;
-  __syncthreads();
-  if (last >= 0) atomicMax(&s.found, last);
-  __syncthreads();
-  found = s.found;
-  __syncthreads();
-  return found;
+__device__ __forceinline__ bool passes(Want want, double target, int count, double mass) {
+  return want == kCount ? (double)count >= target : want == kMassAtLeast ? mass >= target : mass > target;
 }
 
-// The first token of the order whose sums pass: whose count reaches `target`
-// or whose weight reaches or passes it; the row's last token in the bins if
-// none does.  The bins' sums are those of the whole row and are taken again
-// at the end.
+// The first bin with tokens whose sums pass; `end`, the last one with tokens, if none does.
+__device__ __forceinline__ int first_bin(Shared &s, Turn &turn, Want want, double target, int end) {
+  const int b = threadIdx.x, c = s.count[b];
+  const int first = turn.first(c && passes(want, target, s.count_before[b] + c, s.mass_before[b] + s.mass[b]));
+  return first < 0 ? end : first;
+}
+
+__device__ __forceinline__ uint64_t token_of(float l, int i) { return (uint64_t)key_of(l) << 32 | (uint32_t)~i; }
+__device__ __forceinline__ float logit_of(uint64_t token) { return value_of((uint32_t)(token >> 32)); }
+
+// Logits from l0 to l1 are those of bins b0 .. b1 and perhaps a few more.
 template <int DT>
-__device__ Place find_place(Shared &s, const Row<DT> &row, Want want, double target, int bin, int count0,
-                            double mass0) {
+__device__ __forceinline__ void logits_of_bins(const Row<DT> &row, int b0, int b1, float &l0, float &l1) {
+  const float lo = (float)((double)row.top - (double)(b1 + 1) * row.width);
+  l0 = lo > -__builtin_inff() ? value_of(key_of(lo) - 1u) : -__builtin_inff();
+  l1 = row.top;
+  if (b0) {
+    const float hi = (float)((double)row.top - (double)b0 * row.width);
+    l1 = fminf(l1, value_of(key_of(hi) + 1u));
+  }
+}
+
+// The first token of a bin whose sums pass (the bin's last one if none does):
+// its tokens are counted in 1024 equal ranges of their words, then those of
+// the range that passes in as many again, until that holds one.
+// each(f): f(logit, index) for the tokens to look through, the bin's among them.
+template <int DT, typename Each>
+__device__ __forceinline__ Place find_place(Shared &s, Turn &turn, const Row<DT> &row, Want want, double target, int bin, Each each) {
   const int tid = threadIdx.x;
-  const double edge = edge_of(bin);
-  uint32_t prefix = 0;
+  const double edge = s.edge[bin];
+  float l0, l1;
+  logits_of_bins(row, bin, bin, l0, l1);
+  uint64_t low = (uint64_t)key_of(l0) << 32, high = (uint64_t)key_of(l1) << 32 | 0xFFFFFFFFull;
   Place at{};
-  at.count = count0;
-  at.mass = mass0;
-  for (int level = 3; level >= 0; --level) {
-    const int shift = 8 * level;
+  at.count = s.count_before[bin];
+  at.mass = s.mass_before[bin];
+  for (;;) {
+    if (low >> 32 == high >> 32) low = max(low, (low >> 32) << 32 | (uint32_t)~(row.n - 1));
+    const uint64_t span = high - low;
+    const int shift = max(0, 64 - (span ? __builtin_clzll(span) : 63) - 10);
     __syncthreads();
-    for (int i = tid; i < 256; i += kThreads) s.count[i] = 0u, s.mass[i] = 0ull;
+    s.fine_count[tid] = 0;
+    s.fine_mass[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < row.n; i += kThreads) {
-      const float l = row.at(i);
-      const uint32_t key = key_of(l);
-      if (level < 3 && (key >> (shift + 8)) != prefix) continue;
+    each([&](float l, int i) {
+      const uint64_t token = token_of(l, i);
+      if (token < low || token > high) return;
       const double t = row.depth(l);
-      if (bin_of(t) != bin) continue;
-      const int b = 255 - (int)((key >> shift) & 255u);
-      atomicAdd(&s.count[b], 1u);
-      atomicAdd((unsigned long long *)&s.mass[b], (unsigned long long)mass_of(t, bin));
-    }
-    __syncthreads();
-    scan_bins(s, 256, [&](int) { return edge; });
-    const int c0 = at.count;
-    const double m0 = at.mass;
-    const int b = first_bin(s, 256, [&](int b) {
-      if (want == kCount) return (double)(c0 + s.count_before[b] + (int)s.count[b]) >= target;
-      const double m = m0 + (s.mass_before[b] + mass_value(s.mass[b], edge));
-      return want == kMassAtLeast ? m >= target : m > target;
+      if (bin_of(t) != bin) return;
+      const int c = (int)((high - token) >> shift);
+      atomicAdd(&s.fine_count[c], 1);
+      atomicAdd((unsigned long long *)&s.fine_mass[c], (unsigned long long)mass_of(t, bin));
+      s.fine_token[c] = token;
     });
-    at.count = c0 + s.count_before[b];
-    at.mass = m0 + s.mass_before[b];
-    prefix = prefix << 8 | (uint32_t)(255 - b);
-  }
-  // all that is left are equal logits: the n-th of them by index
-  const int equal = (int)s.count[255 - (int)(prefix & 255u)];
-  at.key = prefix;
-  const double t = row.depth(value_of(prefix));
-  at.weight = mass_value(mass_of(t, bin), edge);
-  int nth = equal;
-  if (want == kCount) {
-    nth = (int)target - at.count;
-  } else {
-    // the least n with mass + n weight passing
-    int lo = 1, hi = equal;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      const double m = at.mass + mid * at.weight;
-      if (want == kMassAtLeast ? m >= target : m > target) hi = mid;
-      else lo = mid + 1;
-    }
-    nth = lo;
-  }
-  nth = max(1, min(nth, equal));
-  at.count += nth;
-  at.mass += nth * at.weight;
-  const int lane = tid & 63, wave = tid >> 6;
-  int seen = 0;
-  __syncthreads();
-  if (tid == 0) s.found = -1;
-  for (int i0 = 0; i0 < row.n; i0 += kThreads) {
-    const int i = i0 + tid;
-    const bool same = i < row.n && key_of(row.at(min(i, row.n - 1))) == prefix;
-    const uint64_t who = __ballot(same);
     __syncthreads();
-    if (lane == 0) s.wave_count[wave] = __popcll(who);
+    const int c = s.fine_count[tid];
+    const double m = mass_value(s.fine_mass[tid], edge);
+    int c0, c_all;
+    double m0, m_all;
+    turn.scan(c, m, c0, m0, c_all, m_all);
+    int b = turn.first(c && passes(want, target, at.count + c0 + c, at.mass + (m0 + m)));
+    if (b < 0) b = turn.last(c != 0);
+    // the sums before range b, from the thread that has it (s.sums was last
+    // read before the barrier of first())
+    if (tid == b) s.sums[0][0] = (double)c0, s.sums[1][0] = m0;
     __syncthreads();
-    int before = seen;
-    for (int w = 0; w < kWaves; ++w) {
-      if (w == wave) before = seen;
-      seen += s.wave_count[w];
+    at.count += (int)s.sums[0][0];
+    at.mass += s.sums[1][0];
+    if (s.fine_count[b] == 1) {
+      at.token = s.fine_token[b];
+      at.weight = mass_value(s.fine_mass[b], edge);
+      at.count += 1;
+      at.mass += at.weight;
+      __syncthreads();
+      return at;
     }
-    if (same && before + __popcll(who & ((1ull << lane) - 1)) == nth - 1) s.found = i;
-    if (seen >= nth) break;
+    high -= (uint64_t)b << shift;
+    const uint64_t rest = (1ull << shift) - 1;
+    low = high - low > rest ? high - rest : low;
   }
-  __syncthreads();
-  at.index = s.found;
-  __syncthreads();
-  return at;
 }
 
-// Whether a lies before b in the order, or is it.
-__device__ __forceinline__ bool not_after(const Place &a, const Place &b) {
-  return a.key > b.key || (a.key == b.key && a.index <= b.index);
+// The bins of vectors [v0, v1) of the row, added up over runs of kRun tokens:
+// a thread's own bin; or, for a part of a row, its only run in s.run.
+template <int DT>
+__device__ __forceinline__ void count_bins(Shared &s, const Row<DT> &row, int v0, int v1, bool part, int &count,
+                                           uint64_t &mass) {
+  const int tid = threadIdx.x;
+  constexpr int kStep = kRun / Row<DT>::kVec;
+  for (int a = v0; a < v1; a += kStep) {
+    s.run[tid] = 0;
+    __syncthreads();
+    row.visit(a, min(v1, a + kStep), [&](float l, int) {
+      const double t = row.depth(l);
+      const int b = bin_of(t);
+      if (b < kBins)
+        atomicAdd((unsigned long long *)&s.run[b], (unsigned long long)(mass_of(t, b) + (1ull << kCountShift)));
+    });
+    __syncthreads();
+    if (part) return;
+    count += (int)(s.run[tid] >> kCountShift);
+    mass += s.run[tid] & ((1ull << kCountShift) - 1);
+  }
 }
 
+struct Limits {
+  float u, T, p, m;
+  int k;
+};
+
+__device__ __forceinline__ void answer(const SampleDesc &d, int r, uint64_t token, double weight, double kept) {
+  d.tokens[r] = (int)~(uint32_t)token;
+  if (d.logprobs) d.logprobs[r] = (float)log(weight / kept);
+}
+
+// The row's last token kept and the token drawn, from its bins: a thread's own
+// bin has my_count tokens of my_mass.
+template <int DT>
+__device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row<DT> &row, int r, const Limits &lim, int my_count,
+                       uint64_t my_mass) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  Turn turn{s};
+  int n_all;
+  double z_all;
+  {
+    const double mass = mass_value(my_mass, s.edge[tid]);
+    int c0;
+    double m0;
+    turn.scan(my_count, mass, c0, m0, n_all, z_all);
+    s.count[tid] = my_count;
+    s.mass[tid] = mass;
+    s.count_before[tid] = c0;
+    s.mass_before[tid] = m0;
+  }
+  const double u = lim.u > 0.f ? (double)fminf(lim.u, 0x1.fffffep-1f) : 0.0, p = (double)lim.p;
+  const int k = lim.k;
+  const bool by_k = k > 0 && k < n_all, by_p = lim.p < 1.f;
+  // the depth within which weights are at least m
+  const double deep = lim.m > 0.f ? -kPerNat * log((double)fminf(lim.m, 1.f)) : (double)kBins;
+  const bool by_m = deep < (double)kBins;
+  const int bm = by_m ? (int)deep : 0;
+  const int end = turn.last(my_count != 0);  // (and the arrays above are written)
+
+  // The bins in which the last token kept can lie, [lo, hi], and what is kept
+  // at least and at most: a limit on weights is known to the bins of the
+  // limit before it (and to the sums' rounding).  `wanted`: all bins in which
+  // a place is looked for.
+  constexpr double kLess = 1.0 - 0x1p-40, kMore = 1.0 + 0x1p-40;
+  int lo = end, hi = end;
+  double z_lo = z_all, z_hi = z_all;
+  bool wanted = false;
+  if (by_k) {
+    lo = hi = first_bin(s, turn, kCount, (double)k, end);
+    wanted = tid == hi;
+    z_lo = s.mass_before[hi];
+    z_hi = z_lo + s.mass[hi];
+  }
+#pragma nounroll
+  for (int step = by_p ? 0 : 1; step < 2; ++step) {  // p, then the draw
+    const double f = step ? u : p;
+    const Want want = step ? kMassAbove : kMassAtLeast;
+    if (step && by_m) {
+      wanted |= tid == bm;
+      lo = min(lo, bm);
+      hi = min(hi, bm);
+      z_lo = min(z_lo, s.mass_before[bm]);
+      z_hi = min(z_hi, s.mass_before[bm] + s.mass[bm]);
+    }
+    const int a = first_bin(s, turn, want, f * z_lo * kLess, end);
+    const int b = min(first_bin(s, turn, want, f * z_hi * kMore, end), hi);
+    wanted |= tid >= a && tid <= b;
+    if (!step) {
+      lo = min(lo, a);
+      hi = min(hi, b);
+      z_lo = s.mass_before[lo];
+      z_hi = s.mass_before[hi] + s.mass[hi];
+    }
+  }
+  wanted = wanted && my_count;
+  int place, n;
+  double none;
+  turn.scan(wanted ? my_count : 0, 0.0, place, none, n, none);
+  if (n <= kList) {
+    // gather: logits between the wanted bins' ends, then by their bins
+    const int b0 = turn.first(wanted), b1 = turn.last(wanted);
+    uint32_t *bits = (uint32_t *)s.run;  // a bit for each bin
+    {
+      const uint64_t who = __ballot(wanted);
+      if (lane == 0) s.run[tid >> 6] = who;
+      if (tid == 0) s.listed = 0;
+    }
+    float l0, l1;
+    logits_of_bins(row, b0, b1, l0, l1);
+    __syncthreads();
+    row.visit(0, row.vecs, [&](float l, int i) {
+      if (!(l >= l0 && l <= l1)) return;
+      const int b = bin_of(row.depth(l));
+      if (b < kBins && (bits[b >> 5] >> (b & 31) & 1u)) {
+        const int j = atomicAdd(&s.listed, 1);
+        if (j < kList) s.list[j] = token_of(l, i);
+      }
+    });
+    if (n <= 64) s.fine_count[tid] = place;  // where the bin's tokens begin in the sorted list
+    __syncthreads();
+  }
+  if (n <= 64) {
+    // one wave has all tokens: sorted by counting, every place from a ballot
+    if (tid >= 64) return;
+    const uint64_t e = lane < n ? s.list[lane] : 0;
+    int rank = lane < n ? 0 : lane;
+    for (int i = 0; i < n; ++i) rank += lane < n && lane_value(e, i) > e;
+    s.fine_token[rank] = e;
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    const uint64_t token = s.fine_token[lane];
+    const bool has = lane < n;
+    const double t = has ? row.depth(logit_of(token)) : 0.0;
+    const int bin = bin_of(t), first = has ? s.fine_count[bin] : 0;
+    const double w = has ? mass_value(mass_of(t, bin), s.edge[bin]) : 0.0;
+    const double sum = lane_before(wave_scan(w));  // (the sums before: monotone)
+    const double before = s.mass_before[bin] + (sum - __shfl(sum, first)), upto = before + w;
+    const int count = s.count_before[bin] + lane - first + 1;
+    int kept_count = n_all;
+    double kept = z_all;
+    auto keep = [&](int c, double m) {
+      if (c < kept_count) kept_count = c, kept = m;
+    };
+    if (by_k) {
+      const uint64_t who = __ballot(has && count >= k);
+      if (who) keep(k, lane_value(upto, __builtin_ctzll(who)));
+    }
+    if (by_p) {
+      const uint64_t who = __ballot(has && upto >= p * kept);
+      if (who) {
+        const int j = __builtin_ctzll(who);
+        keep(__builtin_amdgcn_readlane(count, j), lane_value(upto, j));
+      }
+    }
+    if (by_m) {
+      const uint64_t who = __ballot(has && bin == bm && t <= deep);
+      if (who) {
+        const int j = 63 - __builtin_clzll(who);
+        keep(__builtin_amdgcn_readlane(count, j), lane_value(upto, j));
+      } else {
+        keep(s.count_before[bm], s.mass_before[bm]);
+      }
+    }
+    const uint64_t who = __ballot(has && upto > u * kept);
+    if (lane == (who ? __builtin_ctzll(who) : 0)) answer(d, r, token, w, kept);
+    return;
+  }
+  auto each = [&](auto f) {
+    if (n <= kList) {
+      for (int j = tid; j < n; j += kThreads) f(logit_of(s.list[j]), (int)~(uint32_t)s.list[j]);
+    } else {
+      row.visit(0, row.vecs, f);
+    }
+  };
+  Place at{n_all, z_all, 0.0, 0};
+  int kept_count = n_all;
+  double kept = z_all;
+#pragma nounroll
+  for (int step = 0; step < 4; ++step) {
+    double target;
+    Want want = kCount;
+    if (step == 0) {
+      if (!by_k) continue;
+      target = (double)k;
+    } else if (step == 1) {
+      if (!by_p) continue;
+      target = p * kept;
+      want = kMassAtLeast;
+    } else if (step == 2) {
+      if (!by_m) continue;
+      // the tokens of bin bm that are deep enough (of all, where they are not listed)
+      int c = 0;
+      each([&](float l, int) {
+        const double t = row.depth(l);
+        c += bin_of(t) == bm && t <= deep;
+      });
+      int c0;
+      turn.scan(c, 0.0, c0, none, c, none);
+      target = (double)(s.count_before[bm] + c);
+    } else {
+      target = u * kept;
+      want = kMassAbove;
+    }
+    if (want == kCount && target >= (double)kept_count) continue;
+    const int b = first_bin(s, turn, want, target, end);
+    // (the last token of a bin that is kept whole needs no search)
+    if (want == kCount && target == (double)(s.count_before[b] + s.count[b])) {
+      kept_count = (int)target;
+      kept = s.mass_before[b] + s.mass[b];
+      continue;
+    }
+    at = find_place(s, turn, row, want, target, b, each);
+    if (step < 3 && at.count < kept_count) kept_count = at.count, kept = at.mass;
+  }
+  if (tid == 0) answer(d, r, at.token, at.weight, kept);
+}
+
+__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
+
+// The largest logit of vectors [v0, v1) and the lowest index that has it.
+template <int DT>
+__device__ __forceinline__ uint64_t best_of(uint64_t *wave_best, const Row<DT> &row, int v0, int v1) {
+  float top = -__builtin_inff();
+  int at = 0;
+  row.visit(v0, v1, [&](float l, int i) {
+    const bool up = l > top || (l == top && i < at);
+    top = up ? l : top;
+    at = up ? i : at;
+  });
+  uint64_t best = token_of(top, at);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) best = larger(best, __shfl_xor((unsigned long long)best, o));
+  if ((threadIdx.x & 63) == 0) wave_best[threadIdx.x >> 6] = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) best = larger(best, wave_best[w]);
+  return best;
+}
+
+// The vectors of a part: even shares.
+__device__ __forceinline__ int part_begin(int vecs, int part, int parts) {
+  return (int)((int64_t)vecs * part / parts);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void best_kernel(SampleDesc d) {
+  __shared__ uint64_t wave_best[kWaves];
+  const int r = blockIdx.y, part = blockIdx.x;
+  const Row<DT> row(d, r);
+  const uint64_t best = best_of(wave_best, row, part_begin(row.vecs, part, d.parts), part_begin(row.vecs, part + 1, d.parts));
+  if (threadIdx.x == 0) d.best[r * d.parts + part] = best;
+}
+
+// A workgroup a row, or one for each of its parts, of which the last to
+// arrive goes on with all their bins.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void sample_kernel(SampleDesc d) {
   __shared__ Shared s;
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  Row<DT> row;
-  row.p = (const typename MxType<DT>::T *)d.logits + (int64_t)r * d.stride;
-  row.n = d.vocab;
-  // the first token: largest key, then lowest index
+  const int r = blockIdx.y, part = blockIdx.x, tid = threadIdx.x;
+  Row<DT> row(d, r);
+  const Limits lim{d.u[r], d.temperature ? d.temperature[r] : 1.f, d.top_p ? d.top_p[r] : 1.f,
+                   d.min_p ? d.min_p[r] : 0.f, d.top_k ? d.top_k[r] : 0};
+  s.edge[tid] = edge_of(tid);
   uint64_t best = 0;
-  for (int i = tid; i < row.n; i += kThreads) {
-    const uint64_t k = (uint64_t)key_of(row.at(i)) << 32 | (uint32_t)~i;
-    best = k > best ? k : best;
-  }
+  if (d.best) {
+    const int i = tid & 15;
+    best = i < d.parts ? d.best[r * d.parts + i] : 0;
 #pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const uint64_t k = __shfl_xor((unsigned long long)best, o);
-    best = k > best ? k : best;
+    for (int o = 8; o; o >>= 1) best = larger(best, __shfl_xor((unsigned long long)best, o));
+  } else {
+    best = best_of(s.words[0], row, 0, row.vecs);
   }
-  if (lane == 0) s.best[wave] = best;
-  __syncthreads();
-  for (int w = 0; w < kWaves; ++w) best = s.best[w] > best ? s.best[w] : best;
-  row.top = value_of((uint32_t)(best >> 32));
-  const int first = (int)~(uint32_t)best;
-  const float T = d.temperature ? d.temperature[r] : 1.f;
-  const int k = d.top_k ? d.top_k[r] : 0;
-  const float p = d.top_p ? d.top_p[r] : 1.f;
-  const float m = d.min_p ? d.min_p[r] : 0.f;
-  if (row.top == -__builtin_inff()) {
-    if (tid == 0) {
-      d.tokens[r] = -1;
-      if (d.logprobs) d.logprobs[r] = -__builtin_inff();
+  row.top = logit_of(best);
+  const bool none = row.top == -__builtin_inff();
+  if (none || !(lim.T > 0.f) || lim.k == 1) {
+    if (tid == 0 && part == 0) {
+      d.tokens[r] = none ? -1 : (int)~(uint32_t)best;
+      if (d.logprobs) d.logprobs[r] = none ? -__builtin_inff() : 0.f;
     }
     return;
   }
-  if (!(T > 0.f) || k == 1) {
-    if (tid == 0) {
-      d.tokens[r] = first;
-      if (d.logprobs) d.logprobs[r] = 0.f;
+  row.scale = kPerNat / (double)lim.T;
+  row.width = (double)lim.T * (1.0 / kPerNat);
+  int count = 0;
+  uint64_t mass = 0;
+  if (d.parts > 1) {
+    count_bins(s, row, part_begin(row.vecs, part, d.parts), part_begin(row.vecs, part + 1, d.parts), true, count, mass);
+    uint64_t *all = d.bins + (size_t)r * d.parts * kBins + tid;
+    __hip_atomic_store(&all[(size_t)part * kBins], s.run[tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    publish_wait();
+    __syncthreads();
+    if (tid == 0)
+      s.is_last = __hip_atomic_fetch_add(&d.arrived[r], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                  (uint32_t)d.parts - 1;
+    __syncthreads();
+    if (!s.is_last) return;
+    if (tid == 0) __hip_atomic_store(&d.arrived[r], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll 8
+    for (int i = 0; i < d.parts; ++i) {
+      const uint64_t v = __hip_atomic_load(&all[(size_t)i * kBins], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      count += (int)(v >> kCountShift);
+      mass += v & ((1ull << kCountShift) - 1);
     }
-    return;
+  } else {
+    count_bins(s, row, 0, row.vecs, false, count, mass);
   }
-  row.scale = (double)kPerNat / (double)T;
-  auto histogram = [&]() {
-    __syncthreads();
-    for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0u, s.mass[i] = 0ull;
-    __syncthreads();
-    for (int i = tid; i < row.n; i += kThreads) {
-      const double t = row.depth(row.at(i));
-      const int b = bin_of(t);
-      if (b == kBins) continue;
-      atomicAdd(&s.count[b], 1u);
-      atomicAdd((unsigned long long *)&s.mass[b], (unsigned long long)mass_of(t, b));
-    }
-    __syncthreads();
-    scan_bins(s, kBins, [](int b) { return edge_of(b); });
-  };
-  // the last token kept, and what is kept
-  Place last{0u, d.vocab, 0, 0.0, 0.0};
-  histogram();
-  last.count = s.total_count;
-  last.mass = s.total_mass;
-  auto cut = [&](Want want, double target) {
-    const int b = first_bin(s, kBins, [&](int b) {
-      if (want == kCount) return (double)(s.count_before[b] + (int)s.count[b]) >= target;
-      const double mass = s.mass_before[b] + mass_value(s.mass[b], edge_of(b));
-      return want == kMassAtLeast ? mass >= target : mass > target;
-    });
-    const Place at = find_place(s, row, want, target, b, s.count_before[b], s.mass_before[b]);
-    return at;
-  };
-  if (k > 0 && k < last.count) {
-    const Place at = cut(kCount, (double)k);
-    if (not_after(at, last)) last = at;
-    histogram();
+  finish(s, d, row, r, lim, count, mass);
+}
+
+// Parts a row is cut into: one for each CU that would be idle otherwise, of
+// 2048 tokens at least, and at most 8; more where one would be longer than a
+// run (2^18 tokens: 9).
+int parts_of(int rows, int vocab) {
+  const int idle = (256 + rows - 1) / rows, fine = (vocab + 2047) / 2048;
+  if (idle < 2 || fine < 2) return 1;
+  // (a run less what a row's skew and the parts' rounding to vectors may add)
+  const int runs = (vocab + kRun - 33) / (kRun - 32);
+  return std::max(std::min({idle, fine, 8}), runs);
+}
+
+// Whether the row's largest logit is found in a launch of its own: a
+// workgroup of each part reads the whole row for it otherwise.
+bool best_apart(int parts, int vocab, int size) { return parts > 1 && (int64_t)vocab * size > (128 << 10); }
+
+template <int DT>
+hipError_t launch_as(const SampleDesc &d, hipStream_t s) {
+  // (the grid's second extent holds 65535 rows)
+  for (int r0 = 0; r0 < d.rows; r0 += 65535) {
+    SampleDesc e = d;
+    e.rows = min(d.rows - r0, 65535);
+    typedef typename MxType<DT>::T T;
+    e.logits = (const T *)d.logits + (int64_t)r0 * d.stride;
+    e.u += r0;
+    if (e.temperature) e.temperature += r0;
+    if (e.top_k) e.top_k += r0;
+    if (e.top_p) e.top_p += r0;
+    if (e.min_p) e.min_p += r0;
+    e.tokens += r0;
+    if (e.logprobs) e.logprobs += r0;
+    const dim3 grid(e.parts, e.rows), block(kThreads);
+    if (e.best) best_kernel<DT><<<grid, block, 0, s>>>(e);
+    sample_kernel<DT><<<grid, block, 0, s>>>(e);
   }
-  if (p < 1.f) {
-    const Place at = cut(kMassAtLeast, (double)p * last.mass);
-    if (not_after(at, last)) last = at;
-    histogram();
-  }
-  if (m > 0.f) {
-    // how many tokens weigh at least m
-    const double most = -(double)kPerNat * log((double)fminf(m, 1.f));
-    int n = 0;
-    for (int i = tid; i < row.n; i += kThreads) n += row.depth(row.at(i)) <= most;
-#pragma unroll
-    for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o);
-    __syncthreads();
-    if (lane == 0) s.wave_count[wave] = n;
-    __syncthreads();
-    n = 0;
-    for (int w = 0; w < kWaves; ++w) n += s.wave_count[w];
-    __syncthreads();
-    if (n < last.count) {
-      const Place at = cut(kCount, (double)n);
-      last = at;
-      histogram();
-    }
-  }
-  const float u0 = d.u[r];
-  const double u = u0 > 0.f ? (double)fminf(u0, 0x1.fffffep-1f) : 0.0;
-  Place at = cut(kMassAbove, u * last.mass);
-  if (!not_after(at, last)) at = last;
-  if (tid == 0) {
-    d.tokens[r] = at.index;
-    if (d.logprobs) d.logprobs[r] = (float)log(at.weight / last.mass);
-  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t sample_workspace(int, int) { return SPEAR_SAMPLE_HEADER_BYTES; }
+// Of all calls of at most these sizes: fewer rows have more parts.
+size_t sample_workspace(int rows, int vocab) {
+  size_t most = 0;
+  for (int r = 1; r <= min(rows, 255); ++r) most = std::max(most, (size_t)r * parts_of(r, vocab));
+  return SPEAR_SAMPLE_HEADER_BYTES + (most * 8 + 255) / 256 * 256 + most * kBins * 8;
+}
 
-hipError_t launch_sample(const spear_sample_args_t &a, void *, hipStream_t s) {
-  const SampleDesc d{a.logits, a.rows, a.vocab, a.stride, a.u, a.temperature, a.top_p,
-                     a.min_p, a.top_k, a.tokens, a.logprobs};
-  const dim3 grid(a.rows), block(kThreads);
-  if (a.dtype == SPEAR_F16) sample_kernel<0><<<grid, block, 0, s>>>(d);
-  else if (a.dtype == SPEAR_BF16) sample_kernel<1><<<grid, block, 0, s>>>(d);
-  else sample_kernel<2><<<grid, block, 0, s>>>(d);
-  return hipGetLastError();
+hipError_t launch_sample(const spear_sample_args_t &a, void *workspace, hipStream_t s) {
+  SampleDesc d{a.logits, a.rows, a.vocab, parts_of(a.rows, a.vocab), a.stride, a.u, a.temperature, a.top_p,
+               a.min_p, a.top_k, a.tokens, a.logprobs, nullptr, nullptr, nullptr};
+  const size_t n = (size_t)a.rows * d.parts;
+  d.arrived = (uint32_t *)workspace;
+  d.bins = (uint64_t *)((char *)workspace + SPEAR_SAMPLE_HEADER_BYTES);
+  const bool apart = best_apart(d.parts, a.vocab, a.dtype == SPEAR_F32 ? 4 : 2);
+  d.best = apart ? d.bins + n * kBins : nullptr;
+  return a.dtype == SPEAR_F16 ? launch_as<0>(d, s) : a.dtype == SPEAR_BF16 ? launch_as<1>(d, s) : launch_as<2>(d, s);
 }
 
 }  // namespace spear
