@@ -59,7 +59,8 @@ struct Row {
   static constexpr int kAhead = 4;  // loads in flight a thread
   const T *p;
   int n, skew, vecs, first, end;
-  float top;     // the largest logit
+  float floor, cap;     // what is below is never drawn, what is above counts as cap
+  float top;            // the largest logit
   double scale, width;  // 16 / T, and a bin's width in logits
 
   __device__ Row(const SampleDesc &d, int r) {
@@ -69,6 +70,17 @@ struct Row {
     vecs = (n + skew + kVec - 1) / kVec;
     first = skew ? 1 : 0;
     end = (n + skew) / kVec;
+    floor = top = -__builtin_inff();
+    cap = __builtin_inff();
+  }
+  // A row that has logits of +infinity draws from these alone: the others
+  // become -infinity, and they the largest number.
+  __device__ __forceinline__ void set(float best, float T) {
+    if (best == __builtin_inff()) floor = best;
+    cap = 3.402823466e38f;
+    top = fminf(best, cap);
+    scale = kPerNat / (double)T;
+    width = (double)T * (1.0 / kPerNat);
   }
   // f(logit, index) for the logits of vectors [v0, v1), a thread's in
   // ascending order but for those of vectors that reach over the row's ends.
@@ -102,14 +114,14 @@ struct Row {
       if (i < n) f(clean(p[i]), i);
     }
   }
-  static __device__ __forceinline__ float clean(T v) {
+  // NaN (of which no comparison holds) counts as -infinity.
+  __device__ __forceinline__ float clean(T v) const {
     const float l = MxType<DT>::load(v);
-    return l != l ? -__builtin_inff() : l + 0.f;  // (-0 and 0 are one logit)
+    return fminf(l >= floor ? l : -__builtin_inff(), cap);
   }
-  // 16 (top - l) / T; infinite where the logit is never drawn.
+  // 16 (top - l) / T, exactly 0 for the largest; infinite or NaN where the
+  // logit is never drawn.
   __device__ __forceinline__ double depth(float l) const {
-    if (l == top) return 0.0;
-    if (l == -__builtin_inff() || top == __builtin_inff()) return (double)__builtin_inff();
     return ((double)top - (double)l) * scale;
   }
 };
@@ -117,19 +129,18 @@ struct Row {
 __device__ __forceinline__ int bin_of(double t) { return t < (double)kBins ? (int)t : kBins; }
 
 // The weight of a token in its bin, e^(-f / 16) with f = t - b in [0, 1), in
-// units of 2^-32: seven terms leave less than 2^-44.
+// units of 2^-32: six terms of the series leave 2^-33, and adding 2^52
+// rounds to a whole number in the mantissa.
 __device__ __forceinline__ uint64_t mass_of(double t, int b) {
-  const double x = ((double)b - t) * (1.0 / kPerNat);
-  double e = 1.0 / 5040;
-  e = __builtin_fma(e, x, 1.0 / 720);
-  e = __builtin_fma(e, x, 1.0 / 120);
-  e = __builtin_fma(e, x, 1.0 / 24);
-  e = __builtin_fma(e, x, 1.0 / 6);
-  e = __builtin_fma(e, x, 0.5);
-  e = __builtin_fma(e, x, 1.0);
-  e = __builtin_fma(e, x, 1.0);
-  // 2^52 + e 2^32 rounds e 2^32 to a whole number in the mantissa
-  return bitcast<uint64_t>(__builtin_fma(e, 0x1p32, 0x1p52)) & 0xFFFFFFFFFFFFFull;
+  constexpr double x = -1.0 / kPerNat, unit = 0x1p32;
+  const double f = t - (double)b;
+  double e = unit * x * x * x * x * x / 120;
+  e = __builtin_fma(e, f, unit * x * x * x * x / 24);
+  e = __builtin_fma(e, f, unit * x * x * x / 6);
+  e = __builtin_fma(e, f, unit * x * x / 2);
+  e = __builtin_fma(e, f, unit * x);
+  e = __builtin_fma(e, f, unit + 0x1p52);
+  return bitcast<uint64_t>(e) & 0xFFFFFFFFFFFFFull;
 }
 __device__ __forceinline__ double edge_of(int b) { return exp((double)b * (-1.0 / kPerNat)); }
 __device__ __forceinline__ double mass_value(uint64_t m, double edge) { return (double)m * 0x1p-32 * edge; }
@@ -139,11 +150,18 @@ struct Shared {
   int count[kBins], count_before[kBins];
   double mass[kBins], mass_before[kBins], edge[kBins];
   uint64_t list[kList];       // tokens: key << 32 | index inverted, so that they rise against the order
-  int fine_count[kBins];      // finer ranges of a bin
-  uint64_t fine_mass[kBins], fine_token[kBins];
+  int fine_count[kBins];      // finer ranges of a bin's tokens
+  union {
+    struct {
+      uint64_t fine_mass[kBins], fine_token[kBins];
+    };
+    uint64_t buckets[kList];
+  };
   uint64_t words[2][kWaves];  // what waves tell one another, every other time here and there
   double sums[2][kWaves];
-  int listed, is_last;
+  double found_mass, found_weight;
+  uint64_t found_token;
+  int found_count, listed, is_last;
 };
 
 __device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
@@ -255,7 +273,8 @@ __device__ __forceinline__ int first_bin(Shared &s, Turn &turn, Want want, doubl
   return first < 0 ? end : first;
 }
 
-__device__ __forceinline__ uint64_t token_of(float l, int i) { return (uint64_t)key_of(l) << 32 | (uint32_t)~i; }
+// (adding 0 makes one logit of 0 and -0)
+__device__ __forceinline__ uint64_t token_of(float l, int i) { return (uint64_t)key_of(l + 0.f) << 32 | (uint32_t)~i; }
 __device__ __forceinline__ float logit_of(uint64_t token) { return value_of((uint32_t)(token >> 32)); }
 
 // Logits from l0 to l1 are those of bins b0 .. b1 and perhaps a few more.
@@ -266,16 +285,15 @@ __device__ __forceinline__ void logits_of_bins(const Row<DT> &row, int b0, int b
   l1 = row.top;
   if (b0) {
     const float hi = (float)((double)row.top - (double)b0 * row.width);
-    l1 = fminf(l1, value_of(key_of(hi) + 1u));
+    l1 = fminf(l1, value_of(key_of(hi) + 1u));  // (NaN past infinity: l1 stays)
   }
 }
 
 // The first token of a bin whose sums pass (the bin's last one if none does):
 // its tokens are counted in 1024 equal ranges of their words, then those of
 // the range that passes in as many again, until that holds one.
-// each(f): f(logit, index) for the tokens to look through, the bin's among them.
-template <int DT, typename Each>
-__device__ __forceinline__ Place find_place(Shared &s, Turn &turn, const Row<DT> &row, Want want, double target, int bin, Each each) {
+template <int DT>
+__device__ __forceinline__ Place find_place(Shared &s, Turn &turn, const Row<DT> &row, Want want, double target, int bin) {
   const int tid = threadIdx.x;
   const double edge = s.edge[bin];
   float l0, l1;
@@ -292,7 +310,8 @@ __device__ __forceinline__ Place find_place(Shared &s, Turn &turn, const Row<DT>
     s.fine_count[tid] = 0;
     s.fine_mass[tid] = 0;
     __syncthreads();
-    each([&](float l, int i) {
+    row.visit(0, row.vecs, [&](float l, int i) {
+      if (!(l >= l0)) return;
       const uint64_t token = token_of(l, i);
       if (token < low || token > high) return;
       const double t = row.depth(l);
@@ -441,7 +460,9 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
     }
     float l0, l1;
     logits_of_bins(row, b0, b1, l0, l1);
+    s.fine_count[tid] = 0;
     __syncthreads();
+    if (wanted) s.count[tid] = place;  // where the bin's tokens begin in the sorted list
     row.visit(0, row.vecs, [&](float l, int i) {
       if (!(l >= l0 && l <= l1)) return;
       const int b = bin_of(row.depth(l));
@@ -450,61 +471,97 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
         if (j < kList) s.list[j] = token_of(l, i);
       }
     });
-    if (n <= 64) s.fine_count[tid] = place;  // where the bin's tokens begin in the sorted list
     __syncthreads();
-  }
-  if (n <= 64) {
-    // one wave has all tokens: sorted by counting, every place from a ballot
-    if (tid >= 64) return;
-    const uint64_t e = lane < n ? s.list[lane] : 0;
-    int rank = lane < n ? 0 : lane;
-    for (int i = 0; i < n; ++i) rank += lane < n && lane_value(e, i) > e;
-    s.fine_token[rank] = e;
-    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-    const uint64_t token = s.fine_token[lane];
-    const bool has = lane < n;
-    const double t = has ? row.depth(logit_of(token)) : 0.0;
-    const int bin = bin_of(t), first = has ? s.fine_count[bin] : 0;
-    const double w = has ? mass_value(mass_of(t, bin), s.edge[bin]) : 0.0;
-    const double sum = lane_before(wave_scan(w));  // (the sums before: monotone)
-    const double before = s.mass_before[bin] + (sum - __shfl(sum, first)), upto = before + w;
-    const int count = s.count_before[bin] + lane - first + 1;
+    // sort: counted in 1024 equal ranges of their words, then by comparing
+    // with the others of the same range
+    const uint64_t high = token_of(l1, 0), span = high - token_of(l0, row.n - 1);
+    const int shift = max(0, 64 - (span ? __builtin_clzll(span) : 63) - 10);
+    uint64_t e[2];
+    int range[2], slot[2];
+    bool has[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = tid + kThreads * i;
+      has[i] = j < n;
+      e[i] = has[i] ? s.list[j] : 0;
+      range[i] = has[i] ? (int)((high - e[i]) >> shift) : 0;
+      slot[i] = has[i] ? atomicAdd(&s.fine_count[range[i]], 1) : 0;
+    }
+    __syncthreads();
+    int *start = (int *)s.run;  // (the bits have been read)
+    {
+      int c0, c_all;
+      turn.scan(s.fine_count[tid], 0.0, c0, none, c_all, none);
+      start[tid] = c0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      slot[i] += start[range[i]];
+      if (has[i]) s.buckets[slot[i]] = e[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int from = start[range[i]], to = has[i] ? from + s.fine_count[range[i]] : from;
+      int at = from;
+      for (int j = from; j < to; ++j) at += s.buckets[j] > e[i];
+      if (has[i]) s.list[at] = e[i];
+    }
+    __syncthreads();
+    // two neighbours a thread: their numbers in the order, their weights and the sums up to them
+    double t[2], w[2], upto[2];
+    int bin[2], first[2], count[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = 2 * tid + i;
+      has[i] = j < n;
+      e[i] = has[i] ? s.list[j] : 0;
+      t[i] = has[i] ? row.depth(logit_of(e[i])) : 0.0;
+      bin[i] = bin_of(t[i]);
+      first[i] = has[i] ? s.count[bin[i]] : 0;
+      count[i] = s.count_before[bin[i]] + j - first[i] + 1;
+      w[i] = has[i] ? mass_value(mass_of(t[i], bin[i]), s.edge[bin[i]]) : 0.0;
+    }
+    double sum, *sums = (double *)s.buckets;
+    int c0, c_all;
+    turn.scan(0, w[0] + w[1], c0, sum, c_all, none);
+    sums[2 * tid] = sum;
+    sums[2 * tid + 1] = sum + w[0];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      upto[i] = s.mass_before[bin[i]] + ((i ? sum + w[0] : sum) - sums[first[i]]) + w[i];
     int kept_count = n_all;
     double kept = z_all;
+    // the first or last thread with a token for which `pass` holds tells it
+    auto tell = [&](bool is_first, bool a, bool b) {
+      a = a && has[0], b = b && has[1];
+      const int j = is_first ? turn.first(a || b) : turn.last(a || b);
+      if (tid == j) {
+        const int i = is_first ? !a : b;
+        s.found_count = count[i];
+        s.found_mass = upto[i];
+        s.found_weight = w[i];
+        s.found_token = e[i];
+      }
+      __syncthreads();
+      return j >= 0;
+    };
     auto keep = [&](int c, double m) {
       if (c < kept_count) kept_count = c, kept = m;
     };
-    if (by_k) {
-      const uint64_t who = __ballot(has && count >= k);
-      if (who) keep(k, lane_value(upto, __builtin_ctzll(who)));
-    }
-    if (by_p) {
-      const uint64_t who = __ballot(has && upto >= p * kept);
-      if (who) {
-        const int j = __builtin_ctzll(who);
-        keep(__builtin_amdgcn_readlane(count, j), lane_value(upto, j));
-      }
-    }
+    if (by_k && tell(true, count[0] >= k, count[1] >= k)) keep(k, s.found_mass);
+    if (by_p && tell(true, upto[0] >= p * kept, upto[1] >= p * kept)) keep(s.found_count, s.found_mass);
     if (by_m) {
-      const uint64_t who = __ballot(has && bin == bm && t <= deep);
-      if (who) {
-        const int j = 63 - __builtin_clzll(who);
-        keep(__builtin_amdgcn_readlane(count, j), lane_value(upto, j));
-      } else {
-        keep(s.count_before[bm], s.mass_before[bm]);
-      }
+      // deep enough in the bins around the limit; none: what lies before them
+      const bool any = tell(false, bin[0] >= bm && t[0] <= deep, bin[1] >= bm && t[1] <= deep);
+      keep(any ? s.found_count : s.count_before[bm], any ? s.found_mass : s.mass_before[bm]);
     }
-    const uint64_t who = __ballot(has && upto > u * kept);
-    if (lane == (who ? __builtin_ctzll(who) : 0)) answer(d, r, token, w, kept);
+    if (!tell(true, upto[0] > u * kept, upto[1] > u * kept)) tell(false, true, true);
+    if (tid == 0) answer(d, r, s.found_token, s.found_weight, kept);
     return;
   }
-  auto each = [&](auto f) {
-    if (n <= kList) {
-      for (int j = tid; j < n; j += kThreads) f(logit_of(s.list[j]), (int)~(uint32_t)s.list[j]);
-    } else {
-      row.visit(0, row.vecs, f);
-    }
-  };
   Place at{n_all, z_all, 0.0, 0};
   int kept_count = n_all;
   double kept = z_all;
@@ -521,28 +578,16 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
       want = kMassAtLeast;
     } else if (step == 2) {
       if (!by_m) continue;
-      // the tokens of bin bm that are deep enough (of all, where they are not listed)
-      int c = 0;
-      each([&](float l, int) {
-        const double t = row.depth(l);
-        c += bin_of(t) == bm && t <= deep;
-      });
-      int c0;
+      int c = 0, c0;
+      row.visit(0, row.vecs, [&](float l, int) { c += row.depth(l) <= deep; });
       turn.scan(c, 0.0, c0, none, c, none);
-      target = (double)(s.count_before[bm] + c);
+      target = (double)c;
     } else {
       target = u * kept;
       want = kMassAbove;
     }
     if (want == kCount && target >= (double)kept_count) continue;
-    const int b = first_bin(s, turn, want, target, end);
-    // (the last token of a bin that is kept whole needs no search)
-    if (want == kCount && target == (double)(s.count_before[b] + s.count[b])) {
-      kept_count = (int)target;
-      kept = s.mass_before[b] + s.mass[b];
-      continue;
-    }
-    at = find_place(s, turn, row, want, target, b, each);
+    at = find_place(s, turn, row, want, target, first_bin(s, turn, want, target, end));
     if (step < 3 && at.count < kept_count) kept_count = at.count, kept = at.mass;
   }
   if (tid == 0) answer(d, r, at.token, at.weight, kept);
@@ -603,8 +648,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleDesc d) {
   } else {
     best = best_of(s.words[0], row, 0, row.vecs);
   }
-  row.top = logit_of(best);
-  const bool none = row.top == -__builtin_inff();
+  const float top = logit_of(best);
+  const bool none = top == -__builtin_inff();
   if (none || !(lim.T > 0.f) || lim.k == 1) {
     if (tid == 0 && part == 0) {
       d.tokens[r] = none ? -1 : (int)~(uint32_t)best;
@@ -612,8 +657,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleDesc d) {
     }
     return;
   }
-  row.scale = kPerNat / (double)lim.T;
-  row.width = (double)lim.T * (1.0 / kPerNat);
+  row.set(top, lim.T);
   int count = 0;
   uint64_t mass = 0;
   if (d.parts > 1) {
