@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG, "libspear.so")
 
 SOURCES = ("api.hip", "pack.hip", "decode.hip", "decode_w8.hip", "decode_w4.hip", "wide.hip",
            "prefill.hip", "attn_api.hip", "attn_decode.hip", "attn_prefill.hip", "kv_cache.hip",
-           "mx_api.hip", "mx_convert.hip", "mx_linear.hip", "sample.hip")
+           "mx_api.hip", "mx_convert.hip", "mx_linear.hip", "mx_gemm.hip", "sample.hip")
 ARCH = "gfx950"
 
 # Packed fp32 VALU forms are switched off for all device code; hipcc then

@@ -208,8 +208,14 @@ spear_status_t spear_mx_linear(const spear_mx_linear_args_t *a, void *ws, size_t
     const size_t off = tokens_offset(N, K, M);
     const MxDesc s = sizes_of(x_format, M, K);
     x = spear_mx_t{x_format, M, K, at + off, at + off + up256(code_bytes(x_format, s))};
-    const hipError_t e = launch_mx_quantize(a->x, a->x_dtype, a->x_stride, x_format, mx_desc(x), (hipStream_t)stream);
-    if (e != hipSuccess) return hip_status(e, "token quantize launch");
+    if (mx_linear_quantizes(M, K) && aligned(a->x, 16) && a->x_stride % 8 == 0) {
+      d.x16 = (const uint16_t *)a->x;
+      d.x16_dtype = a->x_dtype;
+      d.x16_stride = a->x_stride;
+    } else {
+      const hipError_t e = launch_mx_quantize(a->x, a->x_dtype, a->x_stride, x_format, mx_desc(x), (hipStream_t)stream);
+      if (e != hipSuccess) return hip_status(e, "token quantize launch");
+    }
   }
   d.w = mx_desc(*a->w);
   d.x = mx_desc(x);
@@ -217,6 +223,8 @@ spear_status_t spear_mx_linear(const spear_mx_linear_args_t *a, void *ws, size_t
   d.y = a->y;
   d.y_dtype = a->y_dtype;
   d.y_stride = a->y_stride;
+  const size_t elem = a->y_dtype == SPEAR_F32 ? 4 : 2;
+  d.y_vec = aligned(a->y, 4 * elem) && a->y_stride % 4 == 0;
   return hip_status(launch_mx_linear(d, ws, at + SPEAR_MX_HEADER_BYTES, (hipStream_t)stream), "linear launch");
 }
 

@@ -40,7 +40,15 @@ struct MxLinearDesc {
   void *y;
   int y_dtype;
   int64_t y_stride;
+  // Tokens that the product quantizes itself, or null (then x has them):
+  // 16-byte aligned rows, mx_linear_quantizes.
+  const uint16_t *x16;
+  int x16_dtype;
+  int64_t x16_stride;
+  bool y_vec;  // four neighbouring outputs from a fourth one on are aligned for one store
 };
+hipError_t launch_mx_gemm(const MxLinearDesc &d, hipStream_t s);
+bool mx_linear_quantizes(int tokens, int cols);
 // Bytes of the workspace past the header that the products need for themselves.
 size_t mx_linear_workspace(int n, int k, int m);
 hipError_t launch_mx_linear(const MxLinearDesc &d, void *header, void *work, hipStream_t s);

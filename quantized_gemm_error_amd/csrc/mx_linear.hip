@@ -1,92 +1,207 @@
-// y = x w^T on microscaled operands.
-#include "mx_device.h"
+// y = x w^T on microscaled operands for few tokens: bound by the weights'
+// stream from memory.
+//
+// A workgroup makes 16 NT rows of w times 16 MT tokens; its waves take units
+// of PER 128-column steps in turn, a wave's operands straight from memory (1 KB
+// a load: the matrices lie in memory as the products take them), and their
+// sums meet in LDS, always in the same order.  Up to 16 tokens that come in 16
+// bits are quantized by the waves that use them, while their weights are on
+// the way: four lanes hold a token's 128 columns.
+#include "mx_mfma.h"
 
 namespace spear {
 namespace {
 
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
+// Where the tokens come from: a microscaled matrix, or 16-bit rows.
+constexpr int kFromMx = -1;
 
-// D += A B for one 16x16x128 block: A 16 rows of w (e2m1), B 16 rows of x.
-// Lane l holds row l % 16 of either and the scale byte of its block l / 16;
-// its 32 codes are block l / 16 (e2m1, 16 bytes) or the columns
-// 64 h + 16 (l / 16) .. + 15, h = 0, 1 (e4m3, 32 bytes).  D lands as rows of w
-// 4 * (l / 16) + v, row of x l % 16.  BYTE: the scale's place in its word.
-//
-// With e4m3 the unit drops product bits about 16 places below the largest
-// product, which leaves an error of 1.3e-5 of a typical sum: nothing beside a
-// 16-bit result's rounding, but much beside an fp32 one's.  EXACT takes the
-// codes of 2 and more and those below 2 in two products of their own, none of
-// which loses a bit (4e-8 over 8192 columns, as an fp32 chain).
-template <int XF, int BYTE, bool EXACT>
-__device__ __forceinline__ f32x4_t mx_mfma(u32x4_t w, const u32x4_t (&x)[2], int ws, int xs, f32x4_t c) {
-  const i32x8_t a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-  const i32x8_t b = {(int)x[0][0], (int)x[0][1], (int)x[0][2], (int)x[0][3],
-                     (int)x[1][0], (int)x[1][1], (int)x[1][2], (int)x[1][3]};
-  if constexpr (EXACT && XF == SPEAR_MXFP8) {
-    const i32x8_t big = ((b >> 6) & 0x01010101) * 255;  // bytes whose exponent field is 8 or more
-    c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b & ~big, c, 4, 0, BYTE, ws, BYTE, xs);
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b & big, c, 4, 0, BYTE, ws, BYTE, xs);
-  }
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, XF == SPEAR_MXFP4 ? 4 : 0,
-                                                          BYTE, ws, BYTE, xs);
-}
-
-template <int YT>
-__device__ __forceinline__ void store_y(const MxLinearDesc &d, int m, int n, f32x4_t v) {
-  typedef typename MxType<YT>::T T;
-  if (m >= d.x.rows) return;
-  T *p = (T *)d.y + (int64_t)m * d.y_stride + n;
+// A token's operand of one step from its 16-bit values: lane (r, g) = (lane %
+// 16, lane / 16) has columns 32 g .. (e2m1, its block) or 16 g .. and 64 +
+// 16 g .. (e4m3, halves of blocks g / 2 and 2 + g / 2) in four pieces of 8.
+// bytes: the scales, e2m1's own block's, e4m3's of the two halves.
+template <int DT, int XF>
+__device__ __forceinline__ void quantize_step(const u16x8_t (&raw)[4], u32x4_t (&x)[2], uint32_t &bytes) {
+  float v[4][8];
+  uint32_t m[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (n + j < d.w.rows) p[j] = MxType<YT>::store(v[j]);
-}
-
-// One wave makes 16 x 16 outputs, straight from memory.
-template <int XF, int YT>
-__global__ __launch_bounds__(64) void mx_linear_simple_kernel(MxLinearDesc d) {
-  constexpr int kXTile = XF == SPEAR_MXFP4 ? 1024 : 2048;
-  const int nb = blockIdx.x % d.w.rb, mb = blockIdx.x / d.w.rb;
-  const int lane = threadIdx.x;
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  const uint8_t *w = d.w.codes + (size_t)nb * d.w.kt * 1024 + 16 * lane;
-  const uint8_t *x = d.x.codes + (size_t)mb * d.x.kt * kXTile + 16 * lane;
-  const int *ws = (const int *)d.w.scales + (size_t)nb * d.w.kq * 64 + lane;
-  const int *xs = (const int *)d.x.scales + (size_t)mb * d.x.kq * 64 + lane;
-  auto tile = [&](int t, int sw, int sx, auto byte) {
-    const u32x4_t a = *(const u32x4_t *)(w + (size_t)t * 1024);
-    u32x4_t b[2] = {*(const u32x4_t *)(x + (size_t)t * kXTile), {0u, 0u, 0u, 0u}};
-    if constexpr (XF == SPEAR_MXFP8) b[1] = *(const u32x4_t *)(x + (size_t)t * kXTile + 1024);
-    acc = mx_mfma<XF, decltype(byte)::value, YT == SPEAR_F32>(a, b, sw, sx, acc);
-  };
-  for (int q = 0; q < d.w.kq; ++q) {
-    const int sw = ws[(size_t)q * 64], sx = xs[(size_t)q * 64], n = d.w.kt - 4 * q;
-    tile(4 * q, sw, sx, std::integral_constant<int, 0>());
-    if (n > 1) tile(4 * q + 1, sw, sx, std::integral_constant<int, 1>());
-    if (n > 2) tile(4 * q + 2, sw, sx, std::integral_constant<int, 2>());
-    if (n > 3) tile(4 * q + 3, sw, sx, std::integral_constant<int, 3>());
+  for (int i = 0; i < 4; ++i) {
+    m[i] = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[i][j] = to_f32<DT>(raw[i][j]);
+      m[i] = max(m[i], bitcast<uint32_t>(v[i][j]) & 0x7FFFFFFFu);
+    }
   }
-  store_y<YT>(d, 16 * mb + (lane & 15), 16 * nb + 4 * (lane >> 4), acc);
+  if constexpr (XF == SPEAR_MXFP4) {
+    bytes = mx_scale_byte<XF>(max(max(m[0], m[1]), max(m[2], m[3])));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t q[2];
+      mx_codes<XF>(v[i], bytes, q);
+      x[0][i] = q[0];
+      x[1][i] = 0u;
+    }
+  } else {
+    bytes = 0u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t half = max(m[2 * h], m[2 * h + 1]);
+      const auto both = __builtin_amdgcn_permlane16_swap(half, half, false, false);  // with lane ^ 16
+      const uint32_t byte = mx_scale_byte<XF>(max((uint32_t)both[0], (uint32_t)both[1]));
+      bytes |= byte << (8 * h);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t q[2];
+        mx_codes<XF>(v[2 * h + i], byte, q);
+        x[h][2 * i] = q[0];
+        x[h][2 * i + 1] = q[1];
+      }
+    }
+  }
 }
 
-template <int XF, int YT>
-hipError_t launch_as(const MxLinearDesc &d, hipStream_t s) {
-  mx_linear_simple_kernel<XF, YT><<<dim3((unsigned)d.w.rb * d.x.rb), dim3(64), 0, s>>>(d);
+template <int XF, bool EXACT, int NT, int MT, int WAVES, int PER, int FROM>
+__global__ __launch_bounds__(64 * WAVES) void mx_decode_kernel(MxLinearDesc d) {
+  constexpr int kXPieces = XF == SPEAR_MXFP4 ? 1 : 2;
+  static_assert(FROM == kFromMx || MT == 1, "16 tokens are quantized in place");
+  __shared__ f32x4_t part[WAVES][NT * MT][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * NT, KT = d.w.kt, KQ = d.w.kq;
+  f32x4_t acc[NT][MT];
+  const uint8_t *w[NT], *x[MT];
+  const int *ws[NT], *xs[MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const size_t b = min(n0 + i, d.w.rb - 1);  // (past the last block its results are not stored)
+    w[i] = d.w.codes + b * KT * 1024 + 16 * lane;
+    ws[i] = (const int *)d.w.scales + b * KQ * 64 + lane;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const size_t b = min(j, d.x.rb - 1);
+    x[j] = d.x.codes + b * KT * (1024 * kXPieces) + 16 * lane;
+    xs[j] = (const int *)d.x.scales + b * KQ * 64 + lane;
+  }
+  const int r = lane & 15, g = lane >> 4;
+  const uint16_t *row = d.x16 + (int64_t)r * d.x16_stride + (XF == SPEAR_MXFP4 ? 32 : 16) * g;
+
+  for (int t0 = wave * PER; t0 < KT; t0 += WAVES * PER) {
+    u32x4_t a[PER][NT], b[PER][MT][2];
+    int sa[NT], sb[MT];
+    uint32_t bytes[PER];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sa[i] = __builtin_nontemporal_load(ws[i] + (size_t)(t0 >> 2) * 64);
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const int t = min(t0 + p, KT - 1);  // (a step past the last is not multiplied)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) a[p][i] = __builtin_nontemporal_load((const u32x4_t *)(w[i] + (size_t)t * 1024));
+    }
+    if constexpr (FROM == kFromMx) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j) sb[j] = xs[j][(size_t)(t0 >> 2) * 64];
+#pragma unroll
+      for (int p = 0; p < PER; ++p) {
+        const int t = min(t0 + p, KT - 1);
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            b[p][j][h] = h < kXPieces ? *(const u32x4_t *)(x[j] + (size_t)t * (1024 * kXPieces) + 1024 * h)
+                                      : u32x4_t{0u, 0u, 0u, 0u};
+      }
+    } else {
+      u16x8_t raw[PER][4];
+#pragma unroll
+      for (int p = 0; p < PER; ++p) {
+        const int t = min(t0 + p, KT - 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = 128 * t + (XF == SPEAR_MXFP4 ? 8 * i : 64 * (i >> 1) + 8 * (i & 1));
+          raw[p][i] = r < d.x.rows ? *(const u16x8_t *)(row + at) : u16x8_t{0, 0, 0, 0, 0, 0, 0, 0};
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < PER; ++p) quantize_step<FROM, XF>(raw[p], b[p][0], bytes[p]);
+    }
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      if (t0 + p >= KT) break;
+      const int shift = 8 * ((t0 + p) & 3);
+      int xscale[MT];
+      if constexpr (FROM == kFromMx) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) xscale[j] = sb[j] >> shift;
+      } else if constexpr (XF == SPEAR_MXFP4) {
+        xscale[0] = (int)bytes[p];
+      } else {
+        // block g's byte is half g / 2 of the lanes 2 (g % 2) and the one after
+        xscale[0] = __shfl((int)bytes[p], r + 32 * (g & 1)) >> (8 * (g >> 1));
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          acc[i][j] = mx_mfma<XF, EXACT>(a[p][i], b[p][j], sa[i] >> shift, xscale[j], acc[i][j]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) part[wave][i * MT + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int o = tid; o < NT * MT * 64; o += 64 * WAVES) {
+    const int tile = o >> 6, l = o & 63;
+    f32x4_t v = part[0][tile][l];
+#pragma unroll
+    for (int k = 1; k < WAVES; ++k) v += part[k][tile][l];
+    store_y(d, 16 * (tile % MT) + (l & 15), 16 * (n0 + tile / MT) + 4 * (l >> 4), v);
+  }
+}
+
+template <int XF, bool EXACT, int NT, int MT, int WAVES, int PER>
+hipError_t launch_from(const MxLinearDesc &d, hipStream_t s) {
+  const dim3 grid((d.w.rb + NT - 1) / NT), block(64 * WAVES);
+  if constexpr (MT == 1) {
+    if (d.x16) {
+      if (d.x16_dtype == SPEAR_F16) mx_decode_kernel<XF, EXACT, NT, MT, WAVES, PER, DT_F16><<<grid, block, 0, s>>>(d);
+      else mx_decode_kernel<XF, EXACT, NT, MT, WAVES, PER, DT_BF16><<<grid, block, 0, s>>>(d);
+      return hipGetLastError();
+    }
+  }
+  mx_decode_kernel<XF, EXACT, NT, MT, WAVES, PER, kFromMx><<<grid, block, 0, s>>>(d);
   return hipGetLastError();
 }
 
-template <int XF>
-hipError_t launch_for(const MxLinearDesc &d, hipStream_t s) {
-  return d.y_dtype == SPEAR_F16    ? launch_as<XF, 0>(d, s)
-         : d.y_dtype == SPEAR_BF16 ? launch_as<XF, 1>(d, s)
-                                   : launch_as<XF, 2>(d, s);
+template <int XF, bool EXACT, int MT>
+hipError_t launch_rows(const MxLinearDesc &d, hipStream_t s) {
+  // a workgroup of 16 waves for each block of 16 rows while that is one a CU
+  // at most; two and four blocks a workgroup share what they read of x
+  constexpr int PER = MT == 1 ? 4 : MT == 2 ? 2 : 1;
+  if (d.w.rb <= 256) return launch_from<XF, EXACT, 1, MT, 16, PER>(d, s);
+  if (d.w.rb <= 1024) return launch_from<XF, EXACT, 2, MT, 8, PER>(d, s);
+  return launch_from<XF, EXACT, 4, MT, 8, PER>(d, s);
+}
+
+template <int XF, bool EXACT>
+hipError_t launch_tokens(const MxLinearDesc &d, hipStream_t s) {
+  return d.x.rows <= 16   ? launch_rows<XF, EXACT, 1>(d, s)
+         : d.x.rows <= 32 ? launch_rows<XF, EXACT, 2>(d, s)
+                          : launch_rows<XF, EXACT, 4>(d, s);
 }
 
 }  // namespace
 
 size_t mx_linear_workspace(int, int, int) { return 0; }
 
+bool mx_linear_quantizes(int tokens, int cols) { return tokens <= 16 && cols % 128 == 0; }
+
 hipError_t launch_mx_linear(const MxLinearDesc &d, void *, void *, hipStream_t s) {
-  return d.x_format == SPEAR_MXFP4 ? launch_for<SPEAR_MXFP4>(d, s) : launch_for<SPEAR_MXFP8>(d, s);
+  if (d.x.rows > 64) return launch_mx_gemm(d, s);
+  if (d.x_format == SPEAR_MXFP4) return launch_tokens<SPEAR_MXFP4, false>(d, s);
+  return d.y_dtype == SPEAR_F32 ? launch_tokens<SPEAR_MXFP8, true>(d, s) : launch_tokens<SPEAR_MXFP8, false>(d, s);
 }
 
 }  // namespace spear
