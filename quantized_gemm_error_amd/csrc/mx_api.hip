@@ -225,6 +225,7 @@ spear_status_t spear_mx_linear(const spear_mx_linear_args_t *a, void *ws, size_t
   d.y_stride = a->y_stride;
   const size_t elem = a->y_dtype == SPEAR_F32 ? 4 : 2;
   d.y_vec = aligned(a->y, 4 * elem) && a->y_stride % 4 == 0;
+  d.y_vec16 = aligned(a->y, 16) && a->y_stride * elem % 16 == 0;
   return hip_status(launch_mx_linear(d, ws, at + SPEAR_MX_HEADER_BYTES, (hipStream_t)stream), "linear launch");
 }
 

@@ -45,7 +45,7 @@ struct MxLinearDesc {
   const uint16_t *x16;
   int x16_dtype;
   int64_t x16_stride;
-  bool y_vec;  // four neighbouring outputs from a fourth one on are aligned for one store
+  bool y_vec, y_vec16;  // outputs from a fourth one on are aligned for stores of four, for 16 bytes
 };
 hipError_t launch_mx_gemm(const MxLinearDesc &d, hipStream_t s);
 bool mx_linear_quantizes(int tokens, int cols);

@@ -330,6 +330,31 @@ def test_linear_large(tokens, N, K, xf, out):
     assert off <= 1, float(off)
 
 
+@pytest.mark.parametrize("xf,out", [("fp8", "f16"), ("fp4", "bf16"), ("fp8", "f32")])
+@pytest.mark.parametrize("tokens,N,K", [(1040, 2100, 260), (1100, 6001, 700), (2050, 8200, 520), (129, 28680, 300)])
+def test_linear_many_outputs(tokens, N, K, xf, out):
+    """Each size of tile, with edges in both directions: all outputs against fp32 products, and rows
+    and columns around the edges against the oracle."""
+    note(f"linear {tokens} x {N} x {K} {xf} {out}")
+    x, w = randn(N, (tokens, K), "f16", spread=0.5), randn(K, (N, K), "f16")
+    big = torch.full((tokens, N + 16), 7.0, dtype=DT[out], device="cuda")
+    y = run_linear(w, x, xf, out, y=big[:, 8:N + 8])
+    torch.cuda.synchronize()
+    assert (big[:, :8] == 7).all() and (big[:, N + 8:] == 7).all()
+    rows = np.unique(np.r_[0, 31, 32, 127, 128, tokens - 1, np.arange(tokens - 5, tokens)])
+    cols = np.unique(np.r_[0, 63, 64, 255, 256, np.arange(N - 20, N)])
+    check_linear(y[rows][:, cols], w[cols], x[rows], xf, out, "edges")
+    xv = mx.spear_mx_dequantize(mx.spear_mx_quantize(x.cuda(), xf))
+    wv = mx.spear_mx_dequantize(mx.spear_mx_quantize(w.cuda(), "fp4"))
+    ref, scale = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    off = ((y.float() - ref).abs() / (torch.finfo(DT[out]).eps * ref.abs() + 2.0 ** -12 * scale)).max()
+    assert off <= 1, float(off)
+    del ref, scale
+    again = run_linear(w, x, xf, out)
+    torch.cuda.synchronize()
+    assert torch.equal(again, y)
+
+
 def test_linear_takes_matrices_and_values_alike():
     note("linear forms")
     w = mx.spear_mx_quantize(randn(1, (200, 512), "f16").cuda(), "fp4")
