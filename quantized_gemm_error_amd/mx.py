@@ -131,21 +131,18 @@ class SpearMX:
     def __init__(self, codes, scales, rows: int, cols: int, fmt):
         import torch
         fmt = _format(fmt)
-        lib = _lib()
-        _fits(rows, "rows"), _fits(cols, "cols")
-        need = lib.spear_mx_code_bytes(fmt, rows, cols), lib.spear_mx_scale_bytes(fmt, rows, cols)
-        if rows != 0 and not need[0]:
-            raise SpearError(SPEAR_ERR_INVALID_ARGUMENT, f"invalid sizes {rows} x {cols}")
+        need = _mx_bytes(fmt, rows, cols)
         for t, name, n in ((codes, "codes", need[0]), (scales, "scales", need[1])):
             _require(t.dtype == torch.uint8, f"{name} must be uint8", TypeError)
             _require(t.dim() == 1 and t.is_contiguous() and t.numel() == n,
                      f"{name} must be contiguous, of {n} bytes")
         _require(codes.device == scales.device, f"codes are on {codes.device}, scales on {scales.device}")
-        self.codes, self.scales, self.rows, self.cols, self.format = codes, scales, rows, cols, fmt
-        self.device = codes.device
-        self.shape = (rows, cols)
-        self.spans = _span(codes), _span(scales)
-        self.c = SpearMXC(fmt, rows, cols, codes.data_ptr(), scales.data_ptr())
+        self._parts, self.device = (codes, scales), codes.device
+        self._set(fmt, rows, cols, codes.data_ptr(), scales.data_ptr())
+
+    def _set(self, fmt, rows, cols, codes_at, scales_at):
+        self.rows, self.cols, self.format, self.shape = rows, cols, fmt, (rows, cols)
+        self.c = SpearMXC(fmt, rows, cols, codes_at, scales_at)
         self.at = ctypes.addressof(self.c)
 
     @classmethod
@@ -153,14 +150,41 @@ class SpearMX:
         """A matrix whose values are not set."""
         import torch
         fmt = _format(fmt)
-        lib = _lib()
+        codes, scales = _mx_bytes(fmt, rows, cols)
+        # one allocation: a device's allocations start at 512-byte places, and codes is a multiple of 1024
+        both = torch.empty(codes + scales, dtype=torch.uint8, device=device)
+        self = cls.__new__(cls)
+        self._both, self._parts, self.device = both, None, both.device
+        at = both.data_ptr()
+        self._set(fmt, rows, cols, at, at + codes)
+        return self
+
+    def _tensors(self):
+        if self._parts is None:
+            n = _mx_bytes(self.format, self.rows, self.cols)[0]
+            self._parts = self._both[:n], self._both[n:]
+        return self._parts
+
+    @property
+    def codes(self):
+        return self._tensors()[0]
+
+    @property
+    def scales(self):
+        return self._tensors()[1]
+
+    @property
+    def spans(self):
+        return tuple(_span(t) for t in self._tensors())
+
+
+def _mx_bytes(fmt: int, rows: int, cols: int):
+    """spear_mx_code_bytes and spear_mx_scale_bytes."""
+    if not (0 <= rows <= 1 << 24 and 1 <= cols <= 1 << 20):
         _fits(rows, "rows"), _fits(cols, "cols")
-        a, b = lib.spear_mx_code_bytes(fmt, rows, cols), lib.spear_mx_scale_bytes(fmt, rows, cols)
-        if rows != 0 and not a:
-            raise SpearError(SPEAR_ERR_INVALID_ARGUMENT, f"invalid sizes {rows} x {cols}")
-        # one allocation: a device's allocations start at 512-byte places, and a is a multiple of 1024
-        both = torch.empty(a + b, dtype=torch.uint8, device=device)
-        return cls(both[:a], both[a:], rows, cols, fmt)
+        raise SpearError(SPEAR_ERR_INVALID_ARGUMENT, f"invalid sizes {rows} x {cols}")
+    blocks = (rows + 15) >> 4
+    return blocks * ((cols + 127) >> 7) * (2048 if fmt else 1024), blocks * ((cols + 511) >> 9) * 256
 
 
 def _meets(mx: SpearMX, span) -> bool:
@@ -180,7 +204,7 @@ def spear_mx_quantize(x, fmt="fp4", out: SpearMX = None, stream=None) -> SpearMX
     if out is None:
         out = SpearMX.empty(rows, cols, fmt, device)
         if on.given:
-            on.made(out.codes)
+            on.made(out._both)
     with on as ptr:
         status = _lib().spear_mx_quantize(x.data_ptr(), code, stride, out.at, ptr)
     if status:
@@ -211,6 +235,22 @@ def spear_mx_dequantize(x: SpearMX, dtype=None, out=None, stream=None):
     return out
 
 
+def _norm_overlaps(x, weight, residual, residual_out, out, mx):
+    """An output may lie where x or the residual lies if it is the same rows, and nowhere else."""
+    ins = [(n, t) for n, t in (("x", x), ("weight", weight), ("residual", residual)) if t is not None]
+    outs = [] if residual_out is None else [("residual_out", residual_out)]
+    if mx and out is not None:
+        for name, t in ins + outs:
+            _require(not _meets(out, _span(t)), f"out must not overlap {name}")
+    elif out is not None:
+        outs.append(("out", out))
+    for i, (name, t) in enumerate(outs):
+        for other, u in ins + outs[:i]:
+            if _meet(_span(t), _span(u)):
+                _require(other in ("x", "residual") and _same_rows(t, u),
+                         f"{name} overlaps {other} and is not the same rows")
+
+
 def spear_rms_norm(x, weight, eps: float = 1e-5, residual=None, residual_out=None, out=None,
                    out_format=None, stream=None):
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight over the last dimension of
@@ -223,30 +263,21 @@ def spear_rms_norm(x, weight, eps: float = 1e-5, residual=None, residual_out=Non
     _as(weight, "weight", x.dtype, device, (hidden,))
     _require(residual is not None or residual_out is None, "residual_out without a residual")
     mx = isinstance(out, SpearMX) or (out is None and out_format is not None)
-    ins, outs = [("x", x), ("weight", weight)], []
     r_stride = ro_stride = o_stride = 0
     if residual is not None:
         r_stride = _as(residual, "residual", x.dtype, device, shape)
-        ins.append(("residual", residual))
     if residual_out is not None:
         ro_stride = _as(residual_out, "residual_out", x.dtype, device, shape)
-        outs.append(("residual_out", residual_out))
     if out is not None:
         if mx:
             _require(out.device == device, f"out is on {out.device}, x on {device}")
-            _require(out.shape == (rows, hidden), f"out is {out.shape}, x {(rows, hidden)}")
+            _require(out.shape == shape, f"out is {out.shape}, x {tuple(shape)}")
             _require(out_format is None or _format(out_format) == out.format, "out has another format")
-            for name, t in ins + outs:
-                _require(not _meets(out, _span(t)), f"out must not overlap {name}")
         else:
             _require(out_format is None, "out_format with a 16-bit out")
             o_stride = _as(out, "out", x.dtype, device, shape)
-            outs.append(("out", out))
-    for i, (name, t) in enumerate(outs):
-        for other, u in ins + outs[:i]:
-            if _meet(_span(t), _span(u)):
-                _require(other in ("x", "residual") and _same_rows(t, u),
-                         f"{name} overlaps {other} and is not the same rows")
+    if out is not None or residual_out is not None:
+        _norm_overlaps(x, weight, residual, residual_out, out, mx)
     _gpu(device)
     on = _On(device, stream)
     made = []
@@ -257,7 +288,7 @@ def spear_rms_norm(x, weight, eps: float = 1e-5, residual=None, residual_out=Non
     if out is None:
         if mx:
             out = SpearMX.empty(rows, hidden, out_format, device)
-            made.append(out.codes)
+            made.append(out._both)
         else:
             out = torch.empty(shape, dtype=x.dtype, device=device)
             o_stride = hidden
