@@ -11,8 +11,16 @@
 //
 // A token's weight is held relative to its bin's upper edge as a whole number
 // of 2^-32, so that the sums do not depend on the order of the atomics; a row
-// is counted in runs of at most 2^15 tokens, so that a bin's count and weight
+// is counted in runs of less than 2^16 tokens, so that a bin's count and weight
 // fit one 64-bit LDS atomic.
+//
+// Measured (MI355X): one row of 32000 fp32 logits under k and p 21 us, 64 rows of
+// 131072 bf16 logits under limits of their own 65 to 93 (rows at T = 1.3 under p
+// alone have more tokens in p's bin than LDS lists), 256 rows of 100003 fp32
+// logits without limits 68.  The last reads its 102 MB three times, once from
+// memory (16 us) and twice from the cache (counting, bound by the 64-bit
+// arithmetic, 25 us; gathering, 15 us); the first is a chain of short steps of
+// one workgroup, each fetched and waited for once.
 #include <algorithm>
 
 #include "mx_device.h"
@@ -23,8 +31,8 @@ namespace {
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBins = 1024;  // one a thread
 constexpr double kPerNat = 16.0;
-constexpr int kCountShift = 48;                  // 2^15 tokens of at most 2^32 stay below it
-constexpr int kRun = 1 << 15;                    // tokens in one run
+constexpr int kCountShift = 48;                  // kRun tokens of at most 2^32 stay below it
+constexpr int kRun = (1 << 16) - 16;             // tokens in one run: their number fits 16 bits
 constexpr int kList = 2048;                      // tokens that are gathered at once
 static_assert(kBins == kThreads, "a thread has one bin");
 
@@ -50,13 +58,22 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return bitcast<float>(key ^ (((key >> 31) - 1u) | 0x80000000u));
 }
 
+// Logits from l0 to l1: none as it stands.
+struct Span {
+  float l0 = __builtin_inff(), l1 = -__builtin_inff();
+  __device__ __forceinline__ bool has(float l) const { return l >= l0 && l <= l1; }
+  __device__ __forceinline__ void add(const Span &o) {
+    l0 = fminf(l0, o.l0);
+    l1 = fmaxf(l1, o.l1);
+  }
+};
+
 // A row's logits in vectors of 16 bytes at their aligned places: element 0 is
 // place `skew` of vector 0; vectors first .. end - 1 lie inside the row whole.
 template <int DT>
 struct Row {
   typedef typename MxType<DT>::T T;
   static constexpr int kVec = 16 / sizeof(T);
-  static constexpr int kAhead = 4;  // loads in flight a thread
   const T *p;
   int n, skew, vecs, first, end;
   float floor, cap;     // what is below is never drawn, what is above counts as cap
@@ -82,37 +99,80 @@ struct Row {
     scale = kPerNat / (double)T;
     width = (double)T * (1.0 / kPerNat);
   }
-  // f(logit, index) for the logits of vectors [v0, v1), a thread's in
-  // ascending order but for those of vectors that reach over the row's ends.
-  template <typename F>
-  __device__ __forceinline__ void visit(int v0, int v1, F f) const {
+  // f(values, index of the first) for the whole vectors of [v0, v1), a
+  // thread's in ascending order, and f1(value, index) for those of vectors that
+  // reach over the row's ends: the row's first before, its last after them.
+  // Four loads are in flight a thread.  The loop stays as small as one vector's
+  // code: a row passes each of its parts a few times only, and code that is
+  // fetched for the first time costs more than it does (unrolled four times,
+  // a gather of 131072 logits took up to 35 us).
+  template <typename F, typename F1>
+  __device__ __forceinline__ void visit_raw(int v0, int v1, F f, F1 f1) const {
     const int a = max(v0, first), b = min(v1, end), tid = threadIdx.x;
-    for (int base = a; base < b; base += kAhead * kThreads) {
-      u32x4_t t[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (base + j * kThreads < b)
-          t[j] = *(const u32x4_t *)(p + (min(base + j * kThreads + tid, b - 1) * kVec - skew));
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int w = base + j * kThreads + tid;
-        if (w < b) {
-          T e[kVec];
-          __builtin_memcpy(e, &t[j], 16);
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) f(clean(e[i]), w * kVec - skew + i);
-        }
-      }
-    }
-    // the vectors that are not whole: the first (before `first`) and the last
     if (v0 < first && tid < kVec) {
       const int i = tid - skew;
-      if (i >= 0 && i < n) f(clean(p[i]), i);
+      if (i >= 0 && i < n) f1(p[i], i);
+    }
+    const T *at = p - skew;
+    u32x4_t t[4];
+    if (a < b) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[j] = *(const u32x4_t *)(at + min(a + tid + j * kThreads, b - 1) * kVec);
+    }
+#pragma nounroll
+    for (int v = a + tid; v < b; v += kThreads) {
+      T e[kVec];
+      __builtin_memcpy(e, &t[0], 16);
+      t[0] = t[1], t[1] = t[2], t[2] = t[3];
+      t[3] = *(const u32x4_t *)(at + min(v + 4 * kThreads, b - 1) * kVec);
+      f(e, v * kVec - skew);
     }
     if (v1 == vecs && vecs > max(end, first) && tid < kVec) {
       const int i = (vecs - 1) * kVec - skew + tid;
-      if (i < n) f(clean(p[i]), i);
+      if (i < n) f1(p[i], i);
     }
+  }
+  // f(logit, index) for the logits of vectors [v0, v1), a thread's in ascending order.
+  template <typename F>
+  __device__ __forceinline__ void visit(int v0, int v1, F f) const {
+    visit_raw(
+        v0, v1,
+        [&](const T(&e)[kVec], int i0) {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) f(clean(e[i]), i0 + i);
+        },
+        [&](T v, int i) { f(clean(v), i); });
+  }
+  // f(logit, index) for the row's logits in either of two spans (as set() has
+  // them), which few are: one after the other.
+  template <typename F>
+  __device__ __forceinline__ void visit_few(Span a, Span b, F f) const {
+    if (a.l1 == cap) a.l1 = __builtin_inff();
+    if (b.l1 == cap) b.l1 = __builtin_inff();
+    const auto either = [&](T v) {
+      const float l = MxType<DT>::load(v);
+      return a.has(l) || b.has(l);
+    };
+    visit_raw(
+        0, vecs,
+        [&](const T(&e)[kVec], int i0) {
+          uint32_t in = 0, w[4];
+          __builtin_memcpy(w, e, 16);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) in |= either(e[i]) ? 1u << i : 0u;
+#pragma nounroll
+          for (; in; in &= in - 1) {
+            const int i = __builtin_ctz(in), word = i * (int)sizeof(T) / 4;
+            uint32_t bits = word & 2 ? (word & 1 ? w[3] : w[2]) : (word & 1 ? w[1] : w[0]);
+            if (sizeof(T) == 2 && (i & 1)) bits >>= 16;
+            T v;
+            __builtin_memcpy(&v, &bits, sizeof v);
+            f(clean(v), i0 + i);
+          }
+        },
+        [&](T v, int i) {
+          if (either(v)) f(clean(v), i);
+        });
   }
   // NaN (of which no comparison holds) counts as -infinity.
   __device__ __forceinline__ float clean(T v) const {
@@ -277,50 +337,56 @@ __device__ __forceinline__ int first_bin(Shared &s, Turn &turn, Want want, doubl
 __device__ __forceinline__ uint64_t token_of(float l, int i) { return (uint64_t)key_of(l + 0.f) << 32 | (uint32_t)~i; }
 __device__ __forceinline__ float logit_of(uint64_t token) { return value_of((uint32_t)(token >> 32)); }
 
-// Logits from l0 to l1 are those of bins b0 .. b1 and perhaps a few more.
+// Those of bins b0 .. b1 and perhaps a few more.
 template <int DT>
-__device__ __forceinline__ void logits_of_bins(const Row<DT> &row, int b0, int b1, float &l0, float &l1) {
+__device__ __forceinline__ Span logits_of_bins(const Row<DT> &row, int b0, int b1) {
+  Span s;
   const float lo = (float)((double)row.top - (double)(b1 + 1) * row.width);
-  l0 = lo > -__builtin_inff() ? value_of(key_of(lo) - 1u) : -__builtin_inff();
-  l1 = row.top;
+  s.l0 = lo > -__builtin_inff() ? value_of(key_of(lo) - 1u) : -__builtin_inff();
+  s.l1 = row.top;
   if (b0) {
     const float hi = (float)((double)row.top - (double)b0 * row.width);
-    l1 = fminf(l1, value_of(key_of(hi) + 1u));  // (NaN past infinity: l1 stays)
+    s.l1 = fminf(s.l1, value_of(key_of(hi) + 1u));  // (NaN past infinity: l1 stays)
   }
+  return s;
 }
 
 // The first token of a bin whose sums pass (the bin's last one if none does):
 // its tokens are counted in 1024 equal ranges of their words, then those of
-// the range that passes in as many again, until that holds one.
+// the range that passes in as many again, until that holds one; from the row
+// until few enough are left for LDS.
 template <int DT>
 __device__ __forceinline__ Place find_place(Shared &s, Turn &turn, const Row<DT> &row, Want want, double target, int bin) {
   const int tid = threadIdx.x;
   const double edge = s.edge[bin];
-  float l0, l1;
-  logits_of_bins(row, bin, bin, l0, l1);
-  uint64_t low = (uint64_t)key_of(l0) << 32, high = (uint64_t)key_of(l1) << 32 | 0xFFFFFFFFull;
+  Span span = logits_of_bins(row, bin, bin);
+  uint64_t low = (uint64_t)key_of(span.l0) << 32, high = (uint64_t)key_of(span.l1) << 32 | 0xFFFFFFFFull;
   Place at{};
   at.count = s.count_before[bin];
   at.mass = s.mass_before[bin];
+  int listed = -1;  // tokens left, in s.list; none there yet
   for (;;) {
     if (low >> 32 == high >> 32) low = max(low, (low >> 32) << 32 | (uint32_t)~(row.n - 1));
-    const uint64_t span = high - low;
-    const int shift = max(0, 64 - (span ? __builtin_clzll(span) : 63) - 10);
+    const uint64_t width = high - low;
+    const int shift = max(0, 64 - (width ? __builtin_clzll(width) : 63) - 10);
     __syncthreads();
     s.fine_count[tid] = 0;
     s.fine_mass[tid] = 0;
     __syncthreads();
-    row.visit(0, row.vecs, [&](float l, int i) {
-      if (!(l >= l0)) return;
-      const uint64_t token = token_of(l, i);
+    auto count = [&](uint64_t token) {
       if (token < low || token > high) return;
-      const double t = row.depth(l);
+      const double t = row.depth(logit_of(token));
       if (bin_of(t) != bin) return;
       const int c = (int)((high - token) >> shift);
       atomicAdd(&s.fine_count[c], 1);
       atomicAdd((unsigned long long *)&s.fine_mass[c], (unsigned long long)mass_of(t, bin));
       s.fine_token[c] = token;
-    });
+    };
+    if (listed < 0) {
+      row.visit_few(span, Span(), [&](float l, int i) { count(token_of(l, i)); });
+    } else {
+      for (int j = tid; j < listed; j += kThreads) count(s.list[j]);
+    }
     __syncthreads();
     const int c = s.fine_count[tid];
     const double m = mass_value(s.fine_mass[tid], edge);
@@ -346,6 +412,19 @@ __device__ __forceinline__ Place find_place(Shared &s, Turn &turn, const Row<DT>
     high -= (uint64_t)b << shift;
     const uint64_t rest = (1ull << shift) - 1;
     low = high - low > rest ? high - rest : low;
+    if (listed < 0 && s.fine_count[b] <= kList) {
+      listed = s.fine_count[b];
+      if (tid == 0) s.listed = 0;
+      span.l0 = logit_of(low);
+      span.l1 = logit_of(high);
+      __syncthreads();
+      row.visit_few(span, Span(), [&](float l, int i) {
+        const uint64_t token = token_of(l, i);
+        if (token < low || token > high || bin_of(row.depth(l)) != bin) return;
+        const int j = atomicAdd(&s.listed, 1);
+        if (j < kList) s.list[j] = token;
+      });
+    }
   }
 }
 
@@ -403,10 +482,10 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
   }
   const double u = lim.u > 0.f ? (double)fminf(lim.u, 0x1.fffffep-1f) : 0.0, p = (double)lim.p;
   const int k = lim.k;
-  const bool by_k = k > 0 && k < n_all, by_p = lim.p < 1.f;
+  bool by_k = k > 0 && k < n_all, by_p = lim.p < 1.f;
   // the depth within which weights are at least m
   const double deep = lim.m > 0.f ? -kPerNat * log((double)fminf(lim.m, 1.f)) : (double)kBins;
-  const bool by_m = deep < (double)kBins;
+  bool by_m = deep < (double)kBins;
   const int bm = by_m ? (int)deep : 0;
   const int end = turn.last(my_count != 0);  // (and the arrays above are written)
 
@@ -418,9 +497,11 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
   int lo = end, hi = end;
   double z_lo = z_all, z_hi = z_all;
   bool wanted = false;
+  Span limits, drawn;  // of logits: the bins of k, p and m, and of the draw
   if (by_k) {
     lo = hi = first_bin(s, turn, kCount, (double)k, end);
     wanted = tid == hi;
+    limits.add(logits_of_bins(row, hi, hi));
     z_lo = s.mass_before[hi];
     z_hi = z_lo + s.mass[hi];
   }
@@ -428,8 +509,14 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
   for (int step = by_p ? 0 : 1; step < 2; ++step) {  // p, then the draw
     const double f = step ? u : p;
     const Want want = step ? kMassAbove : kMassAtLeast;
+    if (step && bm > hi) by_m = false;  // the limits before end the row sooner
     if (step && by_m) {
+      if (bm < lo) {  // and here later, wherever they lie in their bins
+        by_k = by_p = wanted = false;
+        limits = Span();
+      }
       wanted |= tid == bm;
+      limits.add(logits_of_bins(row, bm, bm));
       lo = min(lo, bm);
       hi = min(hi, bm);
       z_lo = min(z_lo, s.mass_before[bm]);
@@ -438,6 +525,9 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
     const int a = first_bin(s, turn, want, f * z_lo * kLess, end);
     const int b = min(first_bin(s, turn, want, f * z_hi * kMore, end), hi);
     wanted |= tid >= a && tid <= b;
+    const Span span = logits_of_bins(row, a, b);
+    if (step) drawn = span;
+    else limits.add(span);
     if (!step) {
       lo = min(lo, a);
       hi = min(hi, b);
@@ -450,32 +540,28 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
   double none;
   turn.scan(wanted ? my_count : 0, 0.0, place, none, n, none);
   if (n <= kList) {
-    // gather: logits between the wanted bins' ends, then by their bins
-    const int b0 = turn.first(wanted), b1 = turn.last(wanted);
+    // gather: logits of the two spans, then by their bins
     uint32_t *bits = (uint32_t *)s.run;  // a bit for each bin
     {
       const uint64_t who = __ballot(wanted);
       if (lane == 0) s.run[tid >> 6] = who;
       if (tid == 0) s.listed = 0;
     }
-    float l0, l1;
-    logits_of_bins(row, b0, b1, l0, l1);
     s.fine_count[tid] = 0;
     __syncthreads();
     if (wanted) s.count[tid] = place;  // where the bin's tokens begin in the sorted list
-    row.visit(0, row.vecs, [&](float l, int i) {
-      if (!(l >= l0 && l <= l1)) return;
+    auto list = [&](float l, int i) {
       const int b = bin_of(row.depth(l));
       if (b < kBins && (bits[b >> 5] >> (b & 31) & 1u)) {
         const int j = atomicAdd(&s.listed, 1);
         if (j < kList) s.list[j] = token_of(l, i);
       }
-    });
+    };
+    row.visit_few(limits, drawn, list);
     __syncthreads();
-    // sort: counted in 1024 equal ranges of their words, then by comparing
-    // with the others of the same range
-    const uint64_t high = token_of(l1, 0), span = high - token_of(l0, row.n - 1);
-    const int shift = max(0, 64 - (span ? __builtin_clzll(span) : 63) - 10);
+    // sort: a bin's tokens spread over as many ranges as they are by their
+    // depth in it, then by comparing with the others of the same range
+    const int half = n > kBins;  // (ranges in pairs)
     uint64_t e[2];
     int range[2], slot[2];
     bool has[2];
@@ -484,7 +570,12 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
       const int j = tid + kThreads * i;
       has[i] = j < n;
       e[i] = has[i] ? s.list[j] : 0;
-      range[i] = has[i] ? (int)((high - e[i]) >> shift) : 0;
+      range[i] = 0;
+      if (has[i]) {
+        const double t = row.depth(logit_of(e[i]));
+        const int b = bin_of(t), c = (b + 1 < kBins ? s.count_before[b + 1] : n_all) - s.count_before[b];
+        range[i] = (s.count[b] + min((int)((t - b) * c), c - 1)) >> half;
+      }
       slot[i] = has[i] ? atomicAdd(&s.fine_count[range[i]], 1) : 0;
     }
     __syncthreads();
@@ -505,6 +596,7 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
     for (int i = 0; i < 2; ++i) {
       const int from = start[range[i]], to = has[i] ? from + s.fine_count[range[i]] : from;
       int at = from;
+#pragma unroll 8
       for (int j = from; j < to; ++j) at += s.buckets[j] > e[i];
       if (has[i]) s.list[at] = e[i];
     }
@@ -601,9 +693,8 @@ __device__ __forceinline__ uint64_t best_of(uint64_t *wave_best, const Row<DT> &
   float top = -__builtin_inff();
   int at = 0;
   row.visit(v0, v1, [&](float l, int i) {
-    const bool up = l > top || (l == top && i < at);
-    top = up ? l : top;
-    at = up ? i : at;
+    at = l > top ? i : at;
+    top = l > top ? l : top;
   });
   uint64_t best = token_of(top, at);
 #pragma unroll
@@ -686,7 +777,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleDesc d) {
 
 // Parts a row is cut into: one for each CU that would be idle otherwise, of
 // 2048 tokens at least, and at most 8; more where one would be longer than a
-// run (2^18 tokens: 9).
+// run.
 int parts_of(int rows, int vocab) {
   const int idle = (256 + rows - 1) / rows, fine = (vocab + 2047) / 2048;
   if (idle < 2 || fine < 2) return 1;
