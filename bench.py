@@ -731,16 +731,21 @@ def further_operator_cases(listed):
 
 
 def operators_context(torch, calls):
-    """The cases of perf/operators.py (the paged cache and its attention) and a few chunk calls
-    between them through the library: each case's call on three sets of inputs in turn, `calls` of
-    them in one captured graph; the median time of a call over five replays."""
+    """The cases of perf/operators.py (the paged cache and its attention), a few chunk calls between
+    them, and the cases of perf/more_operators.py (norm, microscaled products, sampling) through the
+    library: each case's call on three sets of inputs in turn, `calls` of them in one captured
+    graph; the median time of a call over five replays."""
     import importlib.util
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
-    ops = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(ops)
-    ops.own = True
     out = {}
-    for case in ops.listed() + further_operator_cases(ops.listed()):
+    cases = []
+    for name in ("operators", "more_operators"):
+        spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", name + ".py"))
+        ops = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ops)
+        ops.own = True
+        listed = ops.listed()
+        cases += [(ops, c) for c in listed + (further_operator_cases(listed) if name == "operators" else [])]
+    for ops, case in cases:
         states = [ops.prepare(case, seed) for seed in (1, 2, 3)]
         for st in states:
             ops.run(st)
@@ -1228,8 +1233,9 @@ def main():
                          "stream) and print it")
     ap.add_argument("--operators", type=int, metavar="CALLS",
                     help="time only the paged cache's operators and its attention (the cases of "
-                         "perf/operators.py and a few chunk calls between them), CALLS calls of "
-                         "each in a graph, and print them")
+                         "perf/operators.py and a few chunk calls between them) and the norm, the "
+                         "microscaled products and the sampling (perf/more_operators.py), CALLS "
+                         "calls of each in a graph, and print them")
     args = ap.parse_args()
     if args.summarize_profiles:
         summarize_profiles(*args.summarize_profiles, out_dir=os.path.join(ROOT, "profiles"))

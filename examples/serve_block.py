@@ -1,12 +1,14 @@
 """One attention block served with libspear: compensated 4-bit projections, a paged cache, chunked
-prompts, forked samples.
+prompts, forked samples, and the end of each step: norm, vocabulary projection, draw.
 
     python examples/serve_block.py
 
 A block is a fused query-key-value projection and an output projection (SpearLayer), with attention
 over the paged cache between them.  The script serves two prompts in chunks (both in one batch),
 forks each into samples that share the prompt's pages, decodes a few tokens of all of them in one
-batch a step, ends some, compacts the pool and goes on.  Random weights and inputs.
+batch a step, ends some, compacts the pool and goes on.  A Head turns a step's output into tokens: the norm of the
+block's output and its input together, in 8 bits, times a microscaled 4-bit vocabulary matrix, and a
+draw under limits that each sequence has of its own.  Random weights and inputs.
 """
 
 from __future__ import annotations
@@ -18,7 +20,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from quantized_gemm_error_amd import attn, spear, synth  # noqa: E402
+from quantized_gemm_error_amd import attn, mx, sampling, spear, synth  # noqa: E402
 
 
 def _ints(v):
@@ -64,8 +66,30 @@ class Block:
         return self._linear(self.out, o.flatten(1)), missing
 
 
-def serve(block, prompts=(300, 217), chunk=128, samples=3, tokens=8, compact_at=4, seed=0):
-    """-> the outputs of the decode steps, [step] of [sequences still running][hidden]."""
+class Head:
+    """From a step's output to its tokens."""
+
+    def __init__(self, hidden=1024, vocab=4000, slots=16, seed=3):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        w = torch.randn((vocab, hidden), generator=gen, device="cuda") * 2 * hidden ** -0.5
+        self.weight = mx.spear_mx_quantize(w, "fp4")
+        self.norm = (1 + 0.1 * torch.randn(hidden, generator=gen, device="cuda")).half()
+        self.draw_ws = sampling.new_sample_workspace(slots, vocab)
+
+    def logits(self, y, x):
+        """fp32 logits of the rows y (the block's output) + x (its input)."""
+        h, _ = mx.spear_rms_norm(y, self.norm, residual=x, out_format="fp8")
+        return mx.spear_mx_linear(self.weight, h, out_dtype=torch.float32)
+
+    def tokens(self, y, x, u, temperature=None, top_k=None, top_p=None, min_p=None):
+        """-> tokens (int32) and the logarithms of their shares, drawn by the numbers u."""
+        return sampling.spear_sample(self.logits(y, x), u, temperature, top_k, top_p, min_p,
+                                     workspace=self.draw_ws, return_logprobs=True)
+
+
+def serve(block, prompts=(300, 217), chunk=128, samples=3, tokens=8, compact_at=4, seed=0, head=None):
+    """-> the outputs of the decode steps, [step] of [sequences still running][hidden]; with a head
+    also the tokens drawn and their logarithms, [step] of a pair."""
     hidden = block.qkv.K
     gen = torch.Generator(device="cuda").manual_seed(seed)
     x = [torch.randn((n, hidden), generator=gen, device="cuda").half() for n in prompts]
@@ -86,7 +110,11 @@ def serve(block, prompts=(300, 217), chunk=128, samples=3, tokens=8, compact_at=
     dst = list(range(P, P + len(src)))
     attn.spear_kv_fork(block.pool, _ints(src), _ints(dst))
     slots, lens = list(range(P)) + dst, list(prompts) + [prompts[i] for i in src]
-    outputs = []
+    outputs, drawn = [], []
+    draws = torch.Generator(device="cuda").manual_seed(seed + 1)
+    n = P + len(dst)
+    limits = [torch.tensor([v[i % len(v)] for i in range(n)], dtype=t, device="cuda") for v, t in
+              (((0.7, 1.0, 0.0), torch.float32), ((50, 0), torch.int32), ((0.95, 1.0, 0.8), torch.float32))]
     for t in range(tokens):
         if t == compact_at:  # the last sample of each prompt ends
             gone = [s for j, s in enumerate(dst) if j % (samples - 1) == samples - 2]
@@ -99,14 +127,18 @@ def serve(block, prompts=(300, 217), chunk=128, samples=3, tokens=8, compact_at=
         y, missing = block.step(xt, _ints(slots), _ints(lens))
         assert int(missing) == 0, "the pool is too small"
         outputs.append(y)
-    return outputs
+        if head is not None:
+            u = torch.rand(n, generator=draws, device="cuda")[slots]
+            drawn.append(head.tokens(y, xt, u, *(v[slots] for v in limits)))
+    return outputs if head is None else (outputs, drawn)
 
 
 def main():
     torch.cuda.set_device(0)
     block = Block()
-    for i, y in enumerate(serve(block)):
-        print(f"decode step {i}: {y.shape[0]} sequences, rms {y.float().square().mean().sqrt().item():.4f}")
+    for i, (y, (tokens, _)) in enumerate(zip(*serve(block, head=Head()))):
+        print(f"decode step {i}: {y.shape[0]} sequences, rms {y.float().square().mean().sqrt().item():.4f}, "
+              f"tokens {tokens.tolist()}")
     used = int((block.pool.refs > 0).sum())
     print(f"{used} of {block.pool.refs.numel()} pages in use, the highest {int((block.pool.refs > 0).nonzero().max())}")
 

@@ -114,13 +114,11 @@ typedef struct spear_mx_linear_args {
 
 /*
  * Workspace bytes that spear_mx_linear needs for this weight and at most
- * n_tokens tokens (of any kind); 0 when an argument is invalid.  256-byte
- * aligned, its first SPEAR_MX_HEADER_BYTES ZEROED ONCE before its first use,
- * left ready by every call; any call on weights that need no more may use it.
- * Calls that may overlap need different ones, and it is not interchangeable
- * with the workspaces of other headers.
+ * n_tokens tokens that come in 16 bits (x_mx needs none: NULL and 0); 0 when
+ * an argument is invalid.  256-byte aligned, with any contents; a call on any
+ * weight that needs no more may use it.  Calls that may overlap need different
+ * ones.
  */
-#define SPEAR_MX_HEADER_BYTES 16384
 size_t spear_mx_workspace_bytes(const spear_mx_t *w, int32_t n_tokens);
 spear_status_t spear_mx_linear(const spear_mx_linear_args_t *args, void *workspace,
                                size_t workspace_bytes, spear_stream_t stream);

@@ -2,6 +2,8 @@
 // host-side validation before any launch.
 #include <math.h>
 
+#include <algorithm>
+
 #include "api_common.h"
 #include "mx_internal.h"
 
@@ -60,8 +62,6 @@ spear_status_t check_workspace(const void *ws, size_t bytes, size_t need) {
   return SPEAR_OK;
 }
 
-size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-
 size_t code_bytes(int32_t format, const MxDesc &d) {
   return (size_t)d.rb * d.kt * (format == SPEAR_MXFP4 ? 1024 : 2048);
 }
@@ -70,10 +70,6 @@ size_t scale_bytes(const MxDesc &d) { return (size_t)d.rb * d.kq * 256; }
 MxDesc sizes_of(int32_t format, int32_t rows, int32_t cols) {
   return mx_desc(spear_mx_t{format, rows, cols, nullptr, nullptr});
 }
-
-// The workspace of a product: the header, the products' own part, then the
-// tokens' codes and scales (when they come in 16 bits).
-size_t tokens_offset(int n, int k, int m) { return SPEAR_MX_HEADER_BYTES + up256(mx_linear_workspace(n, k, m)); }
 
 }  // namespace
 
@@ -163,7 +159,7 @@ spear_status_t spear_rms_norm(const spear_norm_args_t *a, spear_stream_t stream)
 size_t spear_mx_workspace_bytes(const spear_mx_t *w, int32_t n_tokens) {
   if (!w || !valid_sizes(w->format, w->rows, w->cols) || !valid_sizes(SPEAR_MXFP8, n_tokens, w->cols)) return 0;
   const MxDesc x = sizes_of(SPEAR_MXFP8, n_tokens, w->cols);
-  return tokens_offset(w->rows, w->cols, n_tokens) + up256(code_bytes(SPEAR_MXFP8, x)) + up256(scale_bytes(x));
+  return std::max(code_bytes(SPEAR_MXFP8, x) + scale_bytes(x), size_t(256));
 }
 
 spear_status_t spear_mx_linear(const spear_mx_linear_args_t *a, void *ws, size_t ws_bytes, spear_stream_t stream) {
@@ -202,12 +198,10 @@ spear_status_t spear_mx_linear(const spear_mx_linear_args_t *a, void *ws, size_t
   TRY(check_rows("y", a->y, a->y_dtype, a->y_stride, M > 1 ? N : 0));
   if ((int64_t)mx_desc(*a->w).rb * ((M + 15) / 16) >= (1 << 24))
     return fail(SPEAR_ERR_UNSUPPORTED, "%d x %d outputs in one call", M, N);
-  TRY(check_workspace(ws, ws_bytes, spear_mx_workspace_bytes(a->w, M)));
-  char *at = (char *)ws;
   if (!a->x_mx) {
-    const size_t off = tokens_offset(N, K, M);
-    const MxDesc s = sizes_of(x_format, M, K);
-    x = spear_mx_t{x_format, M, K, at + off, at + off + up256(code_bytes(x_format, s))};
+    TRY(check_workspace(ws, ws_bytes, spear_mx_workspace_bytes(a->w, M)));
+    const size_t codes = code_bytes(x_format, sizes_of(x_format, M, K));  // (a multiple of 1024)
+    x = spear_mx_t{x_format, M, K, ws, (char *)ws + codes};
     if (mx_linear_quantizes(M, K) && aligned(a->x, 16) && a->x_stride % 8 == 0) {
       d.x16 = (const uint16_t *)a->x;
       d.x16_dtype = a->x_dtype;
@@ -226,7 +220,7 @@ spear_status_t spear_mx_linear(const spear_mx_linear_args_t *a, void *ws, size_t
   const size_t elem = a->y_dtype == SPEAR_F32 ? 4 : 2;
   d.y_vec = aligned(a->y, 4 * elem) && a->y_stride % 4 == 0;
   d.y_vec16 = aligned(a->y, 16) && a->y_stride * elem % 16 == 0;
-  return hip_status(launch_mx_linear(d, ws, at + SPEAR_MX_HEADER_BYTES, (hipStream_t)stream), "linear launch");
+  return hip_status(launch_mx_linear(d, (hipStream_t)stream), "linear launch");
 }
 
 size_t spear_sample_workspace_bytes(int32_t rows, int32_t vocab) {

@@ -49,9 +49,7 @@ struct MxLinearDesc {
 };
 hipError_t launch_mx_gemm(const MxLinearDesc &d, hipStream_t s);
 bool mx_linear_quantizes(int tokens, int cols);
-// Bytes of the workspace past the header that the products need for themselves.
-size_t mx_linear_workspace(int n, int k, int m);
-hipError_t launch_mx_linear(const MxLinearDesc &d, void *header, void *work, hipStream_t s);
+hipError_t launch_mx_linear(const MxLinearDesc &d, hipStream_t s);
 
 size_t sample_workspace(int rows, int vocab);
 hipError_t launch_sample(const spear_sample_args_t &a, void *workspace, hipStream_t s);

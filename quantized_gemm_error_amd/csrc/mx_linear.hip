@@ -201,11 +201,9 @@ hipError_t launch_tokens(const MxLinearDesc &d, hipStream_t s) {
 
 }  // namespace
 
-size_t mx_linear_workspace(int, int, int) { return 0; }
-
 bool mx_linear_quantizes(int tokens, int cols) { return tokens <= 16 && cols % 128 == 0; }
 
-hipError_t launch_mx_linear(const MxLinearDesc &d, void *, void *, hipStream_t s) {
+hipError_t launch_mx_linear(const MxLinearDesc &d, hipStream_t s) {
   if (d.x.rows > 64) return launch_mx_gemm(d, s);
   if (d.x_format == SPEAR_MXFP4) return launch_tokens<SPEAR_MXFP4, false>(d, s);
   return d.y_dtype == SPEAR_F32 ? launch_tokens<SPEAR_MXFP8, true>(d, s) : launch_tokens<SPEAR_MXFP8, false>(d, s);

@@ -16,7 +16,6 @@ from .spear import SPEAR_ERR_INVALID_ARGUMENT, SpearError, _check, _require
 
 SPEAR_MXFP4, SPEAR_MXFP8 = 0, 1
 SPEAR_F32 = 2
-SPEAR_MX_HEADER_BYTES = 16384
 
 # Every function the header declares, for the export check.
 EXPORTED = (
@@ -313,8 +312,8 @@ def spear_mx_workspace_bytes(w: SpearMX, n_tokens: int) -> int:
 
 
 def new_mx_workspace(w: SpearMX, n_tokens: int):
-    """A 256-byte aligned workspace with a zeroed header for products of w with at most n_tokens."""
-    return _workspace(spear_mx_workspace_bytes(w, n_tokens), SPEAR_MX_HEADER_BYTES, w.device)
+    """A 256-byte aligned workspace for products of w with at most n_tokens 16-bit tokens."""
+    return _workspace(spear_mx_workspace_bytes(w, n_tokens), 0, w.device)
 
 
 def _workspace(n: int, header: int, device):
@@ -337,7 +336,7 @@ def _workspace_args(workspace, device):
 
 def spear_mx_linear(w: SpearMX, x, y=None, x_format="fp8", out_dtype=None, workspace=None, stream=None):
     """y [tokens][N] = x w^T for w [N][K] ("fp4") and x [tokens][K]: a SpearMX, or float16 or
-    bfloat16 values, which are quantized to x_format in the workspace first.  out_dtype: y's
+    bfloat16 values, which are quantized to x_format in the workspace (these need one) first.  out_dtype: y's
     (None: x's, or bfloat16 for a SpearMX)."""
     import torch
     device = w.device

@@ -135,7 +135,7 @@ def test_linear_operands_and_workspace(lib):
     short = _mx(cols=128)
     assert lib.spear_mx_linear(A(_linear(x=None, x_mx=A(short))), 1 << 40, 1 << 40, None) == INVALID
     need = lib.spear_mx_workspace_bytes(A(_W), 3)
-    assert need >= mx.SPEAR_MX_HEADER_BYTES
+    assert need >= lib.spear_mx_code_bytes(1, 3, 256) + lib.spear_mx_scale_bytes(1, 3, 256)
     for ws, n in ((None, need), (1 << 40, need - 1), ((1 << 40) + 64, need)):
         assert lib.spear_mx_linear(A(_linear()), ws, n, None) == WORKSPACE
     assert lib.spear_mx_linear(A(_linear(n_tokens=0)), None, 0, None) == 0
@@ -182,6 +182,7 @@ def test_sizes_grow_with_their_arguments(lib):
             rb, kt, kq = -(-rows // 16), -(-cols // 128), -(-cols // 512)
             assert lib.spear_mx_code_bytes(fmt, rows, cols) == rb * kt * tile
             assert lib.spear_mx_scale_bytes(fmt, rows, cols) == rb * kq * 256
+            assert mx._mx_bytes(fmt, rows, cols) == (rb * kt * tile, rb * kq * 256)
     assert lib.spear_mx_code_bytes(1, 1 << 24, 1 << 20) == (1 << 20) * (1 << 13) * 2048
     for bad in ((2, 4, 4), (0, -1, 4), (0, 4, 0), (0, (1 << 24) + 1, 4)):
         assert lib.spear_mx_code_bytes(*bad) == 0 and lib.spear_mx_scale_bytes(*bad) == 0

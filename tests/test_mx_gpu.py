@@ -418,7 +418,8 @@ def test_linear_workspace_serves_smaller_calls_with_equal_bits():
     for m in (17, 300, 1, 128, 33, 300):
         mx.spear_mx_linear(other, xs[m], workspace=ws)
         assert torch.equal(mx.spear_mx_linear(w, xs[m], workspace=ws), first[m])
-    assert (ws[:mx.SPEAR_MX_HEADER_BYTES] == 0).all()
+    m = mx.spear_mx_quantize(xs[128], "fp8")
+    assert torch.equal(mx.spear_mx_linear(w, m, out_dtype=torch.float16), first[128])  # needs no workspace
     with pytest.raises(spear.SpearError):
         mx.spear_mx_linear(w, xs[300], workspace=ws[:4096])
     with pytest.raises(spear.SpearError):
