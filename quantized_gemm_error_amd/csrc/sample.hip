@@ -362,6 +362,7 @@ __device__ __forceinline__ Place find_place(Shared &s, Turn &turn, const Row<DT>
   Span span = logits_of_bins(row, bin, bin);
   uint64_t low = (uint64_t)key_of(span.l0) << 32, high = (uint64_t)key_of(span.l1) << 32 | 0xFFFFFFFFull;
   Place at{};
+  at.token = token_of(row.top, 0);
   at.count = s.count_before[bin];
   at.mass = s.mass_before[bin];
   int listed = -1;  // tokens left, in s.list; none there yet
@@ -395,6 +396,7 @@ __device__ __forceinline__ Place find_place(Shared &s, Turn &turn, const Row<DT>
     turn.scan(c, m, c0, m0, c_all, m_all);
     int b = turn.first(c && passes(want, target, at.count + c0 + c, at.mass + (m0 + m)));
     if (b < 0) b = turn.last(c != 0);
+    if (b < 0) return at;  // (no token of the bin: it has one)
     // the sums before range b, from the thread that has it (s.sums was last
     // read before the barrier of first())
     if (tid == b) s.sums[0][0] = (double)c0, s.sums[1][0] = m0;
@@ -559,6 +561,7 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
     };
     row.visit_few(limits, drawn, list);
     __syncthreads();
+    n = min(n, s.listed);  // (they are as many as were counted)
     // sort: a bin's tokens spread over as many ranges as they are by their
     // depth in it, then by comparing with the others of the same range
     const int half = n > kBins;  // (ranges in pairs)

@@ -191,7 +191,8 @@ def _meets(mx: SpearMX, span) -> bool:
 
 
 def spear_mx_quantize(x, fmt="fp4", out: SpearMX = None, stream=None) -> SpearMX:
-    """x [rows][cols] (float16, bfloat16 or float32) as a microscaled matrix."""
+    """x [rows][cols] (float16, bfloat16 or float32) as a microscaled matrix (in out's format, when
+    one is given)."""
     code, rows, cols, stride = _matrix(x, "x")
     device = x.device
     if out is not None:
