@@ -4,9 +4,9 @@
 // A workgroup makes 16 NT rows of w times 16 MT tokens; its waves take units
 // of PER 128-column steps in turn, a wave's operands straight from memory (1 KB
 // a load: the matrices lie in memory as the products take them), and their
-// sums meet in LDS, always in the same order.  Up to 16 tokens that come in 16
-// bits are quantized by the waves that use them, while their weights are on
-// the way: four lanes hold a token's 128 columns.
+// sums meet in LDS, always in the same order.  A few tokens that come in 16 bits
+// are quantized by the waves that use them, while their weights are on the way:
+// four lanes hold a token's 128 columns.
 #include "mx_mfma.h"
 
 namespace spear {
@@ -201,7 +201,12 @@ hipError_t launch_tokens(const MxLinearDesc &d, hipStream_t s) {
 
 }  // namespace
 
-bool mx_linear_quantizes(int tokens, int cols) { return tokens <= 16 && cols % 128 == 0; }
+// Every workgroup quantizes the tokens anew, so a launch that does it once pays
+// from longer rows or more tokens on.  us in a graph, in place / apart, one token
+// and 16: 4096 -> 4096 7.1 / 6.9 and 8.8 / 7.8, 4096 -> 1024 6.3 / 6.5 and 8.1 / 7.2,
+// 11008 -> 4096 13.1 / 11.0 and 16.7 / 11.9, 28672 -> 8192 37 / 30 and 49 / 31; a
+// launch less spares a call of its own 2.
+bool mx_linear_quantizes(int tokens, int cols) { return tokens <= 4 && cols <= 4096 && cols % 128 == 0; }
 
 hipError_t launch_mx_linear(const MxLinearDesc &d, hipStream_t s) {
   if (d.x.rows > 64) return launch_mx_gemm(d, s);

@@ -359,7 +359,7 @@ def test_linear_takes_matrices_and_values_alike():
     note("linear forms")
     w = mx.spear_mx_quantize(randn(1, (200, 512), "f16").cuda(), "fp4")
     ws = mx.new_mx_workspace(w, 70)
-    for tokens in (1, 19, 70):
+    for tokens in (1, 19, 70, 5):
         x = randn(tokens, (tokens, 512), "f16").cuda()
         for xf in ("fp4", "fp8"):
             a = mx.spear_mx_linear(w, x, x_format=xf, workspace=ws)
