@@ -209,8 +209,7 @@ __global__ __launch_bounds__(64 * WN * WM, PERSIMD) void mx_gemm_kernel(MxLinear
 #pragma unroll
   for (int t = 0; t < STAGES - 1; ++t)
     if (t < KT) send(t);
-  // Halves of a step (blocks 2 h and 2 h + 1) go from LDS to registers while
-  // the half before is multiplied.
+  // A step's halves, blocks 2 h and 2 h + 1.
   struct Half {
     u32x4_t x[MB][2], w[NB];
     int xs[MB], ws[NB];

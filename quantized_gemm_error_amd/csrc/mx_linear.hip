@@ -63,7 +63,7 @@ __device__ __forceinline__ void quantize_step(const u16x8_t (&raw)[4], u32x4_t (
 template <int XF, bool EXACT, int NT, int MT, int WAVES, int PER, int FROM>
 __global__ __launch_bounds__(64 * WAVES) void mx_decode_kernel(MxLinearDesc d) {
   constexpr int kXPieces = XF == SPEAR_MXFP4 ? 1 : 2;
-  static_assert(FROM == kFromMx || MT == 1, "16 tokens are quantized in place");
+  static_assert(FROM == kFromMx || MT == 1, "one block of tokens is quantized in place");
   __shared__ f32x4_t part[WAVES][NT * MT][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = blockIdx.x * NT, KT = d.w.kt, KQ = d.w.kq;
