@@ -15,7 +15,7 @@
 // fit one 64-bit LDS atomic.
 //
 // Measured (MI355X): one row of 32000 fp32 logits under k and p 21 us, 64 rows of
-// 131072 bf16 logits under limits of their own 65 to 93 (rows at T = 1.3 under p
+// 131072 bf16 logits under limits of their own 45 to 93 (rows at T = 1.3 under p
 // alone have more tokens in p's bin than LDS lists), 256 rows of 100003 fp32
 // logits without limits 68.  The last reads its 102 MB three times, once from
 // memory (16 us) and twice from the cache (counting, bound by the 64-bit
