@@ -220,7 +220,7 @@ struct Shared {
   uint64_t words[2][kWaves];  // what waves tell one another, every other time here and there
   double sums[2][kWaves];
   double found_mass, found_weight;
-  uint64_t found_token;
+  uint64_t found_token;       // the row's first token until another one is found
   int found_count, listed, is_last;
 };
 
@@ -337,16 +337,25 @@ __device__ __forceinline__ int first_bin(Shared &s, Turn &turn, Want want, doubl
 __device__ __forceinline__ uint64_t token_of(float l, int i) { return (uint64_t)key_of(l + 0.f) << 32 | (uint32_t)~i; }
 __device__ __forceinline__ float logit_of(uint64_t token) { return value_of((uint32_t)(token >> 32)); }
 
-// Those of bins b0 .. b1 and perhaps a few more.
+// Those of bins b0 .. b1 and perhaps a few more: all l whose depth() falls
+// into them.  A depth is 16 (top - l) / T to 2^-51 of itself (a difference, 16 / T
+// and a product, each rounded to 2^-53), so an l that is small beside top may
+// lie on either side of a border by as much: around a border at 0 this is far
+// more than a step of l's type.  2^-50 of |top| and of the depth's logits cover
+// it and what is rounded here (b width is exact); the step of one number after
+// that covers the rounding to fp32.  (An infinite T leaves hi NaN and top in l1.)
 template <int DT>
 __device__ __forceinline__ Span logits_of_bins(const Row<DT> &row, int b0, int b1) {
   Span s;
-  const float lo = (float)((double)row.top - (double)(b1 + 1) * row.width);
+  const double top = (double)row.top, past = (double)(b1 + 1) * row.width;
+  const double margin = 0x1p-50 * (__builtin_fabs(top) + past);
+  const float lo = (float)(top - past - margin);
   s.l0 = lo > -__builtin_inff() ? value_of(key_of(lo) - 1u) : -__builtin_inff();
   s.l1 = row.top;
   if (b0) {
-    const float hi = (float)((double)row.top - (double)b0 * row.width);
-    s.l1 = fminf(s.l1, value_of(key_of(hi) + 1u));  // (NaN past infinity: l1 stays)
+    const float hi = (float)(top - (double)b0 * row.width + margin);
+    const float up = value_of(key_of(hi) + 1u);
+    if (up < s.l1) s.l1 = up;
   }
   return s;
 }
@@ -362,7 +371,8 @@ __device__ __forceinline__ Place find_place(Shared &s, Turn &turn, const Row<DT>
   Span span = logits_of_bins(row, bin, bin);
   uint64_t low = (uint64_t)key_of(span.l0) << 32, high = (uint64_t)key_of(span.l1) << 32 | 0xFFFFFFFFull;
   Place at{};
-  at.token = token_of(row.top, 0);
+  at.token = s.found_token;
+  at.weight = 1.0;
   at.count = s.count_before[bin];
   at.mass = s.mass_before[bin];
   int listed = -1;  // tokens left, in s.list; none there yet
@@ -396,7 +406,7 @@ __device__ __forceinline__ Place find_place(Shared &s, Turn &turn, const Row<DT>
     turn.scan(c, m, c0, m0, c_all, m_all);
     int b = turn.first(c && passes(want, target, at.count + c0 + c, at.mass + (m0 + m)));
     if (b < 0) b = turn.last(c != 0);
-    if (b < 0) return at;  // (no token of the bin: it has one)
+    if (b < 0) return at;  // (no token of the bin, which has one: the row's first)
     // the sums before range b, from the thread that has it (s.sums was last
     // read before the barrier of first())
     if (tid == b) s.sums[0][0] = (double)c0, s.sums[1][0] = m0;
@@ -561,10 +571,10 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
     };
     row.visit_few(limits, drawn, list);
     __syncthreads();
-    n = min(n, s.listed);  // (they are as many as were counted)
+    const int half = n > kBins;  // (ranges in pairs)
+    n = min(n, s.listed);        // (as many as were counted)
     // sort: a bin's tokens spread over as many ranges as they are by their
     // depth in it, then by comparing with the others of the same range
-    const int half = n > kBins;  // (ranges in pairs)
     uint64_t e[2];
     int range[2], slot[2];
     bool has[2];
@@ -657,7 +667,7 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
     if (tid == 0) answer(d, r, s.found_token, s.found_weight, kept);
     return;
   }
-  Place at{n_all, z_all, 0.0, 0};
+  Place at{n_all, z_all, s.found_weight, s.found_token};
   int kept_count = n_all;
   double kept = z_all;
 #pragma nounroll
@@ -733,6 +743,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleDesc d) {
   const Limits lim{d.u[r], d.temperature ? d.temperature[r] : 1.f, d.top_p ? d.top_p[r] : 1.f,
                    d.min_p ? d.min_p[r] : 0.f, d.top_k ? d.top_k[r] : 0};
   s.edge[tid] = edge_of(tid);
+  if (tid == 0) s.found_weight = 1.0;
   uint64_t best = 0;
   if (d.best) {
     const int i = tid & 15;
@@ -752,6 +763,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleDesc d) {
     return;
   }
   row.set(top, lim.T);
+  if (tid == 0) s.found_token = best;
   int count = 0;
   uint64_t mass = 0;
   if (d.parts > 1) {
