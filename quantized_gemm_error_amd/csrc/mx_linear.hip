@@ -60,7 +60,7 @@ __device__ __forceinline__ void quantize_step(const u16x8_t (&raw)[4], u32x4_t (
   }
 }
 
-template <int XF, bool EXACT, int NT, int MT, int WAVES, int PER, int FROM>
+template <int XF, int NT, int MT, int WAVES, int PER, int FROM>
 __global__ __launch_bounds__(64 * WAVES) void mx_decode_kernel(MxLinearDesc d) {
   constexpr int kXPieces = XF == SPEAR_MXFP4 ? 1 : 2;
   static_assert(FROM == kFromMx || MT == 1, "one block of tokens is quantized in place");
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(64 * WAVES) void mx_decode_kernel(MxLinearDesc d) {
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < MT; ++j)
-          acc[i][j] = mx_mfma<XF, EXACT>(a[p][i], b[p][j], sa[i] >> shift, xscale[j], acc[i][j]);
+          acc[i][j] = mx_mfma<XF>(a[p][i], b[p][j], sa[i] >> shift, xscale[j], acc[i][j]);
     }
   }
 #pragma unroll
@@ -164,21 +164,21 @@ __global__ __launch_bounds__(64 * WAVES) void mx_decode_kernel(MxLinearDesc d) {
   }
 }
 
-template <int XF, bool EXACT, int NT, int MT, int WAVES, int PER>
+template <int XF, int NT, int MT, int WAVES, int PER>
 hipError_t launch_from(const MxLinearDesc &d, hipStream_t s) {
   const dim3 grid((d.w.rb + NT - 1) / NT), block(64 * WAVES);
   if constexpr (MT == 1) {
     if (d.x16) {
-      if (d.x16_dtype == SPEAR_F16) mx_decode_kernel<XF, EXACT, NT, MT, WAVES, PER, DT_F16><<<grid, block, 0, s>>>(d);
-      else mx_decode_kernel<XF, EXACT, NT, MT, WAVES, PER, DT_BF16><<<grid, block, 0, s>>>(d);
+      if (d.x16_dtype == SPEAR_F16) mx_decode_kernel<XF, NT, MT, WAVES, PER, DT_F16><<<grid, block, 0, s>>>(d);
+      else mx_decode_kernel<XF, NT, MT, WAVES, PER, DT_BF16><<<grid, block, 0, s>>>(d);
       return hipGetLastError();
     }
   }
-  mx_decode_kernel<XF, EXACT, NT, MT, WAVES, PER, kFromMx><<<grid, block, 0, s>>>(d);
+  mx_decode_kernel<XF, NT, MT, WAVES, PER, kFromMx><<<grid, block, 0, s>>>(d);
   return hipGetLastError();
 }
 
-template <int XF, bool EXACT, int MT>
+template <int XF, int MT>
 hipError_t launch_rows(const MxLinearDesc &d, hipStream_t s) {
   // As many blocks of 16 rows a workgroup (which share what it reads of x, and
   // quantizes) as leave one to a CU, 4 at most, and then as few waves as keep
@@ -186,17 +186,17 @@ hipError_t launch_rows(const MxLinearDesc &d, hipStream_t s) {
   // of 4096 6.5 / 7.2 / 7.9, 6144 rows 9.4 / 7.8 / 8.6, 11008 rows 13.0 / 13.0 /
   // 9.5, 28672 rows of 8192 47 / 36 / 28 (4 waves: 26).
   constexpr int PER = MT == 1 ? 4 : MT == 2 ? 2 : 1;
-  if (d.w.rb <= 256) return launch_from<XF, EXACT, 1, MT, 16, PER>(d, s);
-  if (d.w.rb <= 512) return launch_from<XF, EXACT, 2, MT, 8, PER>(d, s);
-  if (d.w.rb <= 1024) return launch_from<XF, EXACT, 4, MT, 8, PER>(d, s);
-  return launch_from<XF, EXACT, 4, MT, 4, PER>(d, s);
+  if (d.w.rb <= 256) return launch_from<XF, 1, MT, 16, PER>(d, s);
+  if (d.w.rb <= 512) return launch_from<XF, 2, MT, 8, PER>(d, s);
+  if (d.w.rb <= 1024) return launch_from<XF, 4, MT, 8, PER>(d, s);
+  return launch_from<XF, 4, MT, 4, PER>(d, s);
 }
 
-template <int XF, bool EXACT>
+template <int XF>
 hipError_t launch_tokens(const MxLinearDesc &d, hipStream_t s) {
-  return d.x.rows <= 16   ? launch_rows<XF, EXACT, 1>(d, s)
-         : d.x.rows <= 32 ? launch_rows<XF, EXACT, 2>(d, s)
-                          : launch_rows<XF, EXACT, 4>(d, s);
+  return d.x.rows <= 16   ? launch_rows<XF, 1>(d, s)
+         : d.x.rows <= 32 ? launch_rows<XF, 2>(d, s)
+                          : launch_rows<XF, 4>(d, s);
 }
 
 }  // namespace
@@ -210,8 +210,7 @@ bool mx_linear_quantizes(int tokens, int cols) { return tokens <= 4 && cols <= 4
 
 hipError_t launch_mx_linear(const MxLinearDesc &d, hipStream_t s) {
   if (d.x.rows > 64) return launch_mx_gemm(d, s);
-  if (d.x_format == SPEAR_MXFP4) return launch_tokens<SPEAR_MXFP4, false>(d, s);
-  return d.y_dtype == SPEAR_F32 ? launch_tokens<SPEAR_MXFP8, true>(d, s) : launch_tokens<SPEAR_MXFP8, false>(d, s);
+  return d.x_format == SPEAR_MXFP4 ? launch_tokens<SPEAR_MXFP4>(d, s) : launch_tokens<SPEAR_MXFP8>(d, s);
 }
 
 }  // namespace spear

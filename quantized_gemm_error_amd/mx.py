@@ -338,7 +338,7 @@ def _workspace_args(workspace, device):
 def spear_mx_linear(w: SpearMX, x, y=None, x_format="fp8", out_dtype=None, workspace=None, stream=None):
     """y [tokens][N] = x w^T for w [N][K] ("fp4") and x [tokens][K]: a SpearMX, or float16 or
     bfloat16 values, which are quantized to x_format in the workspace (these need one) first.  out_dtype: y's
-    (None: x's, or bfloat16 for a SpearMX)."""
+    (None: x's, or bfloat16 for a SpearMX).  The header says how it is summed."""
     import torch
     device = w.device
     _require(x.device == device, f"x is on {x.device}, w on {device}")
