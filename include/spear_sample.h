@@ -37,7 +37,8 @@ extern "C" {
  *
  *   logits       [rows] of vocab values, stride elements apart (>= 0), of
  *                dtype SPEAR_F16, SPEAR_BF16 or SPEAR_F32.
- *   u            [rows]: in [0, 1).  Below: as 0 (NaN too); above: the last token kept.
+ *   u            [rows]: in [0, 1).  Below: as 0 (NaN too); from 1 on: the last token kept (of
+ *                those that weigh e^-64 or more).
  *   temperature  [rows] or NULL (1): T.  Not above 0: the first token is taken, whatever k, p,
  *                min_p and u are.
  *   top_k        [rows] or NULL (0): k.  Not above 0: no limit.

@@ -110,7 +110,10 @@ def sample_ref(logits: np.ndarray, u, temperature=1.0, top_k=0, top_p=1.0, min_p
         kept &= w >= min(min_p, 1.0)
     n = int(kept.sum())
     cum = np.cumsum(w[:n])
-    u = min(max(u, 0.0), 1 - 2.0 ** -24) if u == u else 0.0
+    if u >= 1:  # the last token kept of those that weigh e^-64 or more
+        at = int((kept[:n] & (depth[:n] < 64)).sum()) - 1
+        return int(order[at]), float(np.log(w[at] / cum[-1])), n, 1.0
+    u = max(u, 0.0) if u == u else 0.0
     at = min(int((cum <= u * cum[-1]).sum()), n - 1)
     edges = np.concatenate([cum[:-1], [0.0] if u > 0 else []])
     near = np.min(np.abs(edges / cum[-1] - u), initial=1.0)

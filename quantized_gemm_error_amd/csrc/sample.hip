@@ -492,7 +492,8 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
     s.count_before[tid] = c0;
     s.mass_before[tid] = m0;
   }
-  const double u = lim.u > 0.f ? (double)fminf(lim.u, 0x1.fffffep-1f) : 0.0, p = (double)lim.p;
+  const double u = lim.u > 0.f ? (double)lim.u : 0.0, p = (double)lim.p;
+  const bool to_end = lim.u >= 1.f;  // the last token kept
   const int k = lim.k;
   bool by_k = k > 0 && k < n_all, by_p = lim.p < 1.f;
   // the depth within which weights are at least m
@@ -534,8 +535,14 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
       z_lo = min(z_lo, s.mass_before[bm]);
       z_hi = min(z_hi, s.mass_before[bm] + s.mass[bm]);
     }
-    const int a = first_bin(s, turn, want, f * z_lo * kLess, end);
-    const int b = min(first_bin(s, turn, want, f * z_hi * kMore, end), hi);
+    int a = lo, b = hi;
+    if (step && to_end) {  // (and where m's bin has no token that is kept, in the last bin before)
+      const int before = by_m ? turn.last(my_count != 0 && tid < bm) : -1;
+      if (before >= 0) a = min(a, before);
+    } else {
+      a = first_bin(s, turn, want, f * z_lo * kLess, end);
+      b = min(first_bin(s, turn, want, f * z_hi * kMore, end), hi);
+    }
     wanted |= tid >= a && tid <= b;
     const Span span = logits_of_bins(row, a, b);
     if (step) drawn = span;
@@ -663,7 +670,8 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
       const bool any = tell(false, bin[0] >= bm && t[0] <= deep, bin[1] >= bm && t[1] <= deep);
       keep(any ? s.found_count : s.count_before[bm], any ? s.found_mass : s.mass_before[bm]);
     }
-    if (!tell(true, upto[0] > u * kept, upto[1] > u * kept)) tell(false, true, true);
+    if (to_end) tell(true, count[0] >= kept_count, count[1] >= kept_count);
+    else if (!tell(true, upto[0] > u * kept, upto[1] > u * kept)) tell(false, true, true);
     if (tid == 0) answer(d, r, s.found_token, s.found_weight, kept);
     return;
   }
@@ -687,11 +695,13 @@ __device__ __forceinline__ void finish(Shared &s, const SampleDesc &d, const Row
       row.visit(0, row.vecs, [&](float l, int) { c += row.depth(l) <= deep; });
       turn.scan(c, 0.0, c0, none, c, none);
       target = (double)c;
+    } else if (to_end) {
+      target = (double)kept_count;
     } else {
       target = u * kept;
       want = kMassAbove;
     }
-    if (want == kCount && target >= (double)kept_count) continue;
+    if (step < 3 && want == kCount && target >= (double)kept_count) continue;
     at = find_place(s, turn, row, want, target, first_bin(s, turn, want, target, end));
     if (step < 3 && at.count < kept_count) kept_count = at.count, kept = at.mass;
   }

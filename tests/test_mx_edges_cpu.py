@@ -1,0 +1,17 @@
+"""Pins of the oracle and refusals beside test_mx_oracle.py's and test_mx_cpu.py's (no GPU)."""
+
+import math
+
+import numpy as np
+import pytest
+
+from oracle import mx_ref
+
+
+def test_the_oracle_draws_the_last_token_kept_from_1_on():
+    for u in (1.0, 1.5, math.inf):
+        assert mx_ref.sample_ref(np.array([0.0, -20.0]), u)[:2] == (1, pytest.approx(-20.0))
+        assert mx_ref.sample_ref(np.array([-63.9, 0.0, -64.1, -200.0]), u)[0] == 0
+        assert mx_ref.sample_ref(np.array([0.0, -1.0, -2.0]), u, top_k=2)[0] == 1
+        assert mx_ref.sample_ref(np.array([0.0, -1.0, -2.0]), u, min_p=0.5)[0] == 0
+    assert mx_ref.sample_ref(np.array([0.0, -20.0]), 1 - 2.0 ** -24)[0] == 0
