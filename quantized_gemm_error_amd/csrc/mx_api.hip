@@ -111,7 +111,9 @@ spear_status_t spear_rms_norm(const spear_norm_args_t *a, spear_stream_t stream)
   if (a->rows > kMaxRows || a->hidden > kMaxHidden)
     return fail(SPEAR_ERR_UNSUPPORTED, "rows=%d above %d or hidden=%d above %d", a->rows, kMaxRows, a->hidden, kMaxHidden);
   if (!(a->eps >= 0) || !isfinite(a->eps)) return fail(SPEAR_ERR_INVALID_ARGUMENT, "eps is negative or not finite");
-  if (!a->out == !a->out_mx) return fail(SPEAR_ERR_INVALID_ARGUMENT, "one of out and out_mx must be given");
+  // (no rows: an empty array may have no address)
+  if ((a->out && a->out_mx) || (a->rows > 0 && !a->out && !a->out_mx))
+    return fail(SPEAR_ERR_INVALID_ARGUMENT, "one of out and out_mx must be given");
   if (!a->residual != !a->residual_out)
     return fail(SPEAR_ERR_INVALID_ARGUMENT, "residual and residual_out come together");
   if (a->out_mx) {

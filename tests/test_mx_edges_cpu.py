@@ -6,6 +6,9 @@ import numpy as np
 import pytest
 
 from oracle import mx_ref
+from test_mx_cpu import A, INVALID, _mx, _norm, lib  # noqa: F401
+
+torch = pytest.importorskip("torch")
 
 
 def test_the_oracle_draws_the_last_token_kept_from_1_on():
@@ -15,3 +18,11 @@ def test_the_oracle_draws_the_last_token_kept_from_1_on():
         assert mx_ref.sample_ref(np.array([0.0, -1.0, -2.0]), u, top_k=2)[0] == 1
         assert mx_ref.sample_ref(np.array([0.0, -1.0, -2.0]), u, min_p=0.5)[0] == 0
     assert mx_ref.sample_ref(np.array([0.0, -20.0]), 1 - 2.0 ** -24)[0] == 0
+
+
+def test_a_norm_of_no_rows_needs_no_addresses(lib):  # noqa: F811
+    for kw in (dict(), dict(residual=None, residual_out=None)):
+        assert lib.spear_rms_norm(A(_norm(rows=0, x=None, out=None, **kw)), None) == 0
+        assert lib.spear_rms_norm(A(_norm(rows=1, out=None, **kw)), None) == INVALID
+    m = _mx(rows=0, codes=None, scales=None)
+    assert lib.spear_rms_norm(A(_norm(rows=0, out_mx=A(m))), None) == INVALID   # two outputs
