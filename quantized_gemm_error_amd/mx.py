@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 
 from . import spear
-from .attn import _fits, _gpu, _meet, _On, _span
+from .attn import _INT32_MAX, _fits, _gpu, _meet, _On, _span
 from .spear import SPEAR_ERR_INVALID_ARGUMENT, SpearError, _check, _require
 
 SPEAR_MXFP4, SPEAR_MXFP8 = 0, 1
@@ -97,6 +97,8 @@ def _matrix(t, name: str, f32: bool = True):
     """t is [rows][cols] with contiguous columns -> its type's code, sizes and row stride."""
     _require(t.dim() == 2, f"{name} must be [rows][cols], got {t.dim()}-D")
     rows, cols = t.shape
+    if rows > _INT32_MAX or cols > _INT32_MAX:
+        _fits(rows, f"rows of {name}"), _fits(cols, f"columns of {name}")
     stride, inner = t.stride()
     if cols > 1 and inner != 1:
         raise ValueError(f"the rows of {name} must be contiguous")

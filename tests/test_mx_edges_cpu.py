@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import mx_ref
+from quantized_gemm_error_amd import mx, sampling
 from test_mx_cpu import A, INVALID, _mx, _norm, lib  # noqa: F401
 
 torch = pytest.importorskip("torch")
@@ -26,3 +27,16 @@ def test_a_norm_of_no_rows_needs_no_addresses(lib):  # noqa: F811
         assert lib.spear_rms_norm(A(_norm(rows=1, out=None, **kw)), None) == INVALID
     m = _mx(rows=0, codes=None, scales=None)
     assert lib.spear_rms_norm(A(_norm(rows=0, out_mx=A(m))), None) == INVALID   # two outputs
+
+
+def test_sizes_past_32_bits_are_refused():
+    """They would reach the library cut to their low 32 bits."""
+    n = 2 ** 32 + 1
+    row = torch.zeros((1, 64), dtype=torch.float16)
+    tall = row.expand(n, 64)
+    w = mx.SpearMX.empty(8, 64, "fp4", "cpu")
+    for call in (lambda: mx.spear_rms_norm(tall, row[0]), lambda: mx.spear_rms_norm(tall, row[0], out_format="fp8"),
+                 lambda: mx.spear_mx_quantize(tall), lambda: mx.spear_mx_linear(w, tall),
+                 lambda: sampling.spear_sample(tall, torch.zeros(1).expand(n))):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
