@@ -40,3 +40,15 @@ def test_sizes_past_32_bits_are_refused():
                  lambda: sampling.spear_sample(tall, torch.zeros(1).expand(n))):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_one_row_in_place_whatever_its_stride():
+    """A stride between rows says nothing where there is one row (the C ABI takes it so)."""
+    big, w = torch.zeros((3, 128), dtype=torch.float16), torch.zeros(64, dtype=torch.float16)
+    x = big[:1, :64]
+    same = x.as_strided((1, 64), (64, 1))
+    for kw in (dict(out=same), dict(residual=same, residual_out=x), dict(residual=x, residual_out=same, out=None)):
+        with pytest.raises(ValueError, match="GPU"):   # every check before the device's passes
+            mx.spear_rms_norm(x, w, **kw)
+    with pytest.raises(ValueError, match="overlaps"):
+        mx.spear_rms_norm(big[:2, :64], w, out=big.as_strided((2, 64), (64, 1)))
