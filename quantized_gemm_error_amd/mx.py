@@ -192,19 +192,20 @@ def _meets(mx: SpearMX, span) -> bool:
     return _meet(mx.spans[0], span) or _meet(mx.spans[1], span)
 
 
-def spear_mx_quantize(x, fmt="fp4", out: SpearMX = None, stream=None) -> SpearMX:
-    """x [rows][cols] (float16, bfloat16 or float32) as a microscaled matrix (in out's format, when
-    one is given)."""
+def spear_mx_quantize(x, fmt=None, out: SpearMX = None, stream=None) -> SpearMX:
+    """x [rows][cols] (float16, bfloat16 or float32) as a microscaled matrix of format fmt (None:
+    out's, or "fp4")."""
     code, rows, cols, stride = _matrix(x, "x")
     device = x.device
     if out is not None:
         _require(out.device == device, f"out is on {out.device}, x on {device}")
         _require(out.shape == (rows, cols), f"out is {out.shape}, x {(rows, cols)}")
+        _require(fmt is None or _format(fmt) == out.format, "out has another format")
         _require(not _meets(out, _span(x)), "out must not overlap x")
     _gpu(device)
     on = _On(device, stream)
     if out is None:
-        out = SpearMX.empty(rows, cols, fmt, device)
+        out = SpearMX.empty(rows, cols, "fp4" if fmt is None else fmt, device)
         if on.given:
             on.made(out._both)
     with on as ptr:

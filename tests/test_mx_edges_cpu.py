@@ -52,3 +52,18 @@ def test_one_row_in_place_whatever_its_stride():
             mx.spear_rms_norm(x, w, **kw)
     with pytest.raises(ValueError, match="overlaps"):
         mx.spear_rms_norm(big[:2, :64], w, out=big.as_strided((2, 64), (64, 1)))
+
+
+def test_a_format_that_is_not_outs_is_refused():
+    x = torch.zeros((4, 64), dtype=torch.float16)
+    for fmt, other in (("fp4", "fp8"), ("fp8", "fp4")):
+        m = mx.SpearMX.empty(4, 64, fmt, "cpu")
+        with pytest.raises(ValueError, match="another format"):
+            mx.spear_mx_quantize(x, other, out=m)
+        with pytest.raises(ValueError, match="format"):
+            mx.spear_mx_quantize(x, "int4", out=m)
+        for given in (fmt, None):
+            with pytest.raises(ValueError, match="GPU"):
+                mx.spear_mx_quantize(x, given, out=m)
+    with pytest.raises(ValueError, match="GPU"):
+        mx.spear_mx_quantize(x)
