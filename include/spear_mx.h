@@ -120,8 +120,8 @@ typedef struct spear_mx_linear_args {
  * Workspace bytes that spear_mx_linear needs for this weight and at most
  * n_tokens tokens that come in 16 bits (x_mx needs none: NULL and 0); 0 when
  * an argument is invalid.  256-byte aligned, with any contents; a call on any
- * weight that needs no more may use it.  Calls that may overlap need different
- * ones.
+ * weight that needs no more may use it.  It overlaps nothing that the call reads
+ * or writes; calls that may overlap need different ones.
  */
 size_t spear_mx_workspace_bytes(const spear_mx_t *w, int32_t n_tokens);
 spear_status_t spear_mx_linear(const spear_mx_linear_args_t *args, void *workspace,

@@ -62,8 +62,8 @@ typedef struct spear_sample_args {
 /*
  * Workspace bytes that spear_sample needs for at most these sizes; 0 when one
  * is invalid.  256-byte aligned, its first SPEAR_SAMPLE_HEADER_BYTES ZEROED
- * ONCE before its first use, left ready by every call.  Calls that may
- * overlap need different ones.
+ * ONCE before its first use, left ready by every call.  It overlaps nothing
+ * that the call reads or writes; calls that may overlap need different ones.
  */
 #define SPEAR_SAMPLE_HEADER_BYTES 16384
 size_t spear_sample_workspace_bytes(int32_t rows, int32_t vocab);

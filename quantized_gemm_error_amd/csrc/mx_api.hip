@@ -62,6 +62,18 @@ spear_status_t check_workspace(const void *ws, size_t bytes, size_t need) {
   return SPEAR_OK;
 }
 
+// Whether `bytes` from p on lie in the `need` bytes of the workspace, which the call writes.
+spear_status_t check_apart(const char *name, const void *p, size_t bytes, const void *ws, size_t need) {
+  const uintptr_t a = (uintptr_t)p, w = (uintptr_t)ws;
+  if (p && a < w + need && w < a + bytes)
+    return fail(SPEAR_ERR_INVALID_ARGUMENT, "%s overlaps the workspace", name);
+  return SPEAR_OK;
+}
+// Bytes from the first to the last element of rows of cols elements.
+size_t row_bytes(int32_t rows, int64_t stride, int32_t cols, int32_t dtype) {
+  return ((size_t)(rows - 1) * stride + cols) * (dtype == SPEAR_F32 ? 4 : 2);
+}
+
 size_t code_bytes(int32_t format, const MxDesc &d) {
   return (size_t)d.rb * d.kt * (format == SPEAR_MXFP4 ? 1024 : 2048);
 }
@@ -201,7 +213,12 @@ spear_status_t spear_mx_linear(const spear_mx_linear_args_t *a, void *ws, size_t
   if ((int64_t)mx_desc(*a->w).rb * ((M + 15) / 16) >= (1 << 24))
     return fail(SPEAR_ERR_UNSUPPORTED, "%d x %d outputs in one call", M, N);
   if (!a->x_mx) {
-    TRY(check_workspace(ws, ws_bytes, spear_mx_workspace_bytes(a->w, M)));
+    const size_t need = spear_mx_workspace_bytes(a->w, M);
+    TRY(check_workspace(ws, ws_bytes, need));
+    TRY(check_apart("x", a->x, row_bytes(M, a->x_stride, K, a->x_dtype), ws, need));
+    TRY(check_apart("y", a->y, row_bytes(M, a->y_stride, N, a->y_dtype), ws, need));
+    TRY(check_apart("w", a->w->codes, code_bytes(SPEAR_MXFP4, mx_desc(*a->w)), ws, need));
+    TRY(check_apart("w", a->w->scales, scale_bytes(mx_desc(*a->w)), ws, need));
     const size_t codes = code_bytes(x_format, sizes_of(x_format, M, K));  // (a multiple of 1024)
     x = spear_mx_t{x_format, M, K, ws, (char *)ws + codes};
     if (mx_linear_quantizes(M, K) && aligned(a->x, 16) && a->x_stride % 8 == 0) {
@@ -243,6 +260,9 @@ spear_status_t spear_sample(const spear_sample_args_t *a, void *ws, size_t ws_by
       !aligned(a->min_p, 4) || !aligned(a->tokens, 4) || !aligned(a->logprobs, 4))
     return fail(SPEAR_ERR_INVALID_ARGUMENT, "the per-row arrays must be 4-byte aligned");
   TRY(check_workspace(ws, ws_bytes, need));
+  TRY(check_apart("logits", a->logits, row_bytes(a->rows, a->stride, a->vocab, a->dtype), ws, need));
+  const void *const per_row[] = {a->u, a->temperature, a->top_k, a->top_p, a->min_p, a->tokens, a->logprobs};
+  for (const void *p : per_row) TRY(check_apart("a per-row array", p, (size_t)a->rows * 4, ws, need));
   return hip_status(launch_sample(*a, ws, (hipStream_t)stream), "sample launch");
 }
 

@@ -7,7 +7,7 @@ import pytest
 
 from oracle import mx_ref
 from quantized_gemm_error_amd import mx, sampling
-from test_mx_cpu import A, INVALID, _mx, _norm, lib  # noqa: F401
+from test_mx_cpu import _W, A, INVALID, _linear, _mx, _norm, _sample, lib  # noqa: F401
 
 torch = pytest.importorskip("torch")
 
@@ -67,3 +67,20 @@ def test_a_format_that_is_not_outs_is_refused():
                 mx.spear_mx_quantize(x, given, out=m)
     with pytest.raises(ValueError, match="GPU"):
         mx.spear_mx_quantize(x)
+
+
+def test_a_workspace_over_an_operand_is_refused(lib):  # noqa: F811
+    at, need = 1 << 40, lib.spear_mx_workspace_bytes(A(_W), 3)
+    for kw in (dict(x=at + need - 2), dict(x=at - 512 * 2 - 510), dict(y=at), dict(y=at - 2 * 64 * 2 - 126),
+               dict(w=_mx(codes=at)), dict(w=_mx(scales=at - 256))):
+        held = kw.get("w")
+        if held is not None:
+            kw = dict(w=A(held))
+        assert lib.spear_mx_linear(A(_linear(**kw)), at, need, None) == INVALID, kw
+        assert b"workspace" in lib.spear_last_error()
+    need = lib.spear_sample_workspace_bytes(4, 1000)
+    for kw in (dict(logits=at + need - 4), dict(logits=at - 4 * 4000 + 4), dict(logits=at, stride=0), dict(u=at - 12),
+               dict(temperature=at), dict(top_k=at + 64), dict(top_p=at + 4), dict(min_p=at + need - 4),
+               dict(tokens=at), dict(logprobs=at - 4)):
+        assert lib.spear_sample(A(_sample(**kw)), at, need, None) == INVALID, kw
+        assert b"workspace" in lib.spear_last_error()
