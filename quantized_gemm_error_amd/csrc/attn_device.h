@@ -153,9 +153,9 @@ __device__ __forceinline__ u32x4_t buffer_words(const void *p, int bytes) {
 // step are wave-uniform).  Bytes past the buffer's range read as zeros.
 // Written out because the compiler waits for every such load before any later
 // LDS read; the caller waits (wait_for_lds_loads) before a barrier instead.  The block
-// writes no register but m0, which nothing else in these kernels uses; the
-// wait states are those of a scalar register that a vector instruction may
-// have written just before (the first load) and of m0.
+// writes no register but m0; the wait states are those of a scalar register
+// that a vector instruction may have written just before (the first load) and
+// of m0.
 template <int N>
 __device__ __forceinline__ void load_to_lds(u32x4_t buffer, uint32_t lds, int even, int odd, int step) {
   static_assert(N == 2 || N == 4, "loads");
@@ -167,7 +167,7 @@ __device__ __forceinline__ void load_to_lds(u32x4_t buffer, uint32_t lds, int ev
         "buffer_load_dwordx4 %2, %3, %4 offen lds"
         :
         : "s"(lds), "v"(even), "v"(odd), "s"(buffer), "s"(step)
-        : "memory", "scc");
+        : "memory", "scc", "m0");
   } else {
     asm volatile(
         "s_mov_b32 m0, %0\n\ts_nop 4\n\t"
@@ -180,7 +180,7 @@ __device__ __forceinline__ void load_to_lds(u32x4_t buffer, uint32_t lds, int ev
         "buffer_load_dwordx4 %2, %3, %6 offen lds"
         :
         : "s"(lds), "v"(even), "v"(odd), "s"(buffer), "s"(step), "s"(2 * step), "s"(3 * step)
-        : "memory", "scc");
+        : "memory", "scc", "m0");
   }
 }
 

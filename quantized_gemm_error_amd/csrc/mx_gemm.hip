@@ -62,18 +62,17 @@ __device__ __forceinline__ u32x4_t buffer_words(const void *p) {
 }
 
 // 16 bytes a lane from byte `at` (a lane's) + step (uniform) of a buffer to
-// LDS byte lds + 16 lane, N times to LDS 1 KB further on each.  Written out
-// because the compiler waits for such a load before any later LDS read.  The
-// block writes no register but m0, which nothing else in these kernels uses;
-// the first wait states are those of a scalar register that a vector
-// instruction may have written just before.
+// LDS byte lds + 16 lane.  Written out because the compiler waits for such a
+// load before any later LDS read.  The block writes no register but m0; the
+// wait states are those of a scalar register that a vector instruction may
+// have written just before.
 __device__ __forceinline__ void load_piece(u32x4_t buffer, uint32_t lds, int at, int step) {
   asm volatile(
       "s_mov_b32 m0, %0\n\ts_nop 4\n\t"
       "buffer_load_dwordx4 %1, %2, %3 offen lds"
       :
       : "s"(lds), "v"(at), "s"(buffer), "s"(step)
-      : "memory");
+      : "memory", "m0");
 }
 
 // At most N of this wave's loads are still in flight, then a barrier; LDS
