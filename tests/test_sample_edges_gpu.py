@@ -1,9 +1,13 @@
 """Sampling where it can go wrong beside test_sample_gpu.py's cases: tokens that lie on a bin's border
-but for the rounding of their depth, and draws at the end of what is kept."""
+but for the rounding of their depth, draws at the end of what is kept, and rows and vocabularies that
+are counted in several runs, parts or launches."""
 
 import numpy as np
 import pytest
 
+from gpu_helpers import note
+from oracle import mx_ref
+from quantized_gemm_error_amd import sampling
 from test_sample_gpu import DT, INF, us, verify
 
 torch = pytest.importorskip("torch")
@@ -76,3 +80,52 @@ def test_the_last_token_kept_where_the_limits_bin_has_none():
         l = torch.tensor([[0.0, -0.001 * depth, -depth, -depth - 0.001, -30.0]] * 3)
         for limits in (dict(), dict(top_k=4), dict(top_p=0.999999)):
             verify(l.cuda(), [1.0, 0.99, 0.2], f"none in the limit's bin {m} {limits}", min_p=m, **limits)
+
+
+def check_rows(logits, rows, what, u, temperature, top_k, top_p, min_p):
+    """A call on all rows with limits of their own; the given rows against the oracle (as verify())."""
+    note(what)
+    n = logits.shape[0]
+    ws = sampling.new_sample_workspace(n, logits.shape[1])
+    tokens, logprobs = sampling.spear_sample(logits, u, temperature, top_k, top_p, min_p, workspace=ws,
+                                             return_logprobs=True)
+    torch.cuda.synchronize()
+    for r in rows:
+        asks = [float(t[r]) for t in (u, temperature, top_k, top_p, min_p)]
+        t, lp, kept, near = mx_ref.sample_ref(logits[r].float().cpu().numpy(), asks[0], asks[1], int(asks[2]), *asks[3:])
+        assert near > 1e-9 or asks[0] == 0, f"{what} row {r}: the draw is at a border ({near})"
+        got, glp = int(tokens[r]), float(logprobs[r])
+        assert got == t, f"{what} row {r}: token {got} for {t} of {kept}"
+        assert abs(glp - lp) <= 1e-9 + 2.0 ** -24 * abs(lp), f"{what} row {r}: {glp} for {lp}"
+    assert (ws[:sampling.SPEAR_SAMPLE_HEADER_BYTES] == 0).all()
+
+
+def asks_of(n, seed):
+    gen = torch.Generator().manual_seed(seed)
+    pick = lambda v, t=torch.float32: torch.tensor(v, dtype=t)[torch.randint(0, len(v), (n,), generator=gen)].cuda()  # noqa: E731
+    return (torch.rand(n, generator=gen).cuda(), pick([1.0, 1.0, 0.7, 1.5, 0.0]),
+            pick([0, 0, 0, 50, 3000], torch.int32), pick([1.0, 1.0, 0.9, 0.5]), pick([0.0, 0.0, 0.01]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab", [(256, 65519), (256, 65520), (256, 65521), (257, 131073), (256, 2 ** 18), (255, 131072),
+                                     (200, 2 ** 18), (129, 100003), (128, 2 ** 18 - 1)])
+def test_rows_counted_in_several_runs_or_parts(n, vocab, dtype):
+    """From 256 rows on one workgroup counts a row in runs of 65520 tokens; fewer rows have as many
+    parts at least.  Rows that start at every place of a 16-byte vector; a flat row among them."""
+    gen = torch.Generator(device="cuda").manual_seed(vocab)
+    pad = 8 * (vocab // 8) + 8 + 3                      # odd: each row starts elsewhere in its vector
+    big = (2 * torch.randn((n, pad), generator=gen, device="cuda")).to(DT[dtype])
+    l = big[:, 1:1 + vocab]
+    l[7] = 0.25
+    rows = sorted({0, 1, 2, 3, 7, n // 2, n - 2, n - 1} | set(range(8, n, max(1, n // 8))))
+    check_rows(l, rows, f"{n} rows of {vocab} {dtype}", *asks_of(n, vocab + n))
+
+
+@pytest.mark.parametrize("n", [65535, 65536, 65600, 131075])
+def test_more_rows_than_a_grid_holds(n):
+    """Rows past the grid's second extent go in launches of their own, each with its arrays' places."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    l = (3 * torch.randn((n, 67), generator=gen, device="cuda")).bfloat16()[:, :65]
+    at = {0, 1, 65533, 65534, 65535, 65536, 65537, 131069, 131070, 131071, n - 2, n - 1} | set(range(0, n, n // 60))
+    check_rows(l, sorted(r for r in at if r < n), f"{n} rows", *asks_of(n, n))
