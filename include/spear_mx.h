@@ -24,7 +24,8 @@ extern "C" {
  * The element formats: 32 consecutive values of a row share a power of two
  * (a byte, exponent + 127) and are held as
  *   SPEAR_MXFP4  e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives,
- *   SPEAR_MXFP8  e4m3: 3 fraction bits, at most 448, steps of 2^-9 below 2^-6.
+ *   SPEAR_MXFP8  e4m3: 3 fraction bits, at most 448, steps of 2^-9 below 2^-6
+ *                (its codes 0x7F and 0xFF, which quantizing never makes, are NaN).
  * Quantizing takes the power 2^(floor(log2 max|v|) - top), top 2 (fp4) or 8
  * (fp8), not below 2^-127, and rounds v over it to nearest even, saturating.
  * A block of zeros has byte 0.  A block with a value that is not finite has

@@ -58,7 +58,9 @@ __device__ __forceinline__ float e2m1_value(uint32_t code) {
 }
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
   const uint32_t e = (code >> 3) & 15u, m = code & 7u;
-  const float v = e ? bitcast<float>((e + 120u) << 23 | m << 20) : 0x1p-9f * (float)m;
+  const float v = (code & 127u) == 127u ? bitcast<float>(0x7FC00000u)  // (as the products read it)
+                  : e                   ? bitcast<float>((e + 120u) << 23 | m << 20)
+                                        : 0x1p-9f * (float)m;
   return code & 128u ? -v : v;
 }
 
