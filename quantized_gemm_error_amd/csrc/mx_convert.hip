@@ -56,12 +56,11 @@ __device__ __forceinline__ float e2m1_value(uint32_t code) {
   const float v = m < 2u ? 0.5f * (float)m : bitcast<float>(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
   return code & 8u ? -v : v;
 }
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  const uint32_t e = (code >> 3) & 15u, m = code & 7u;
-  const float v = (code & 127u) == 127u ? bitcast<float>(0x7FC00000u)  // (as the products read it)
-                  : e                   ? bitcast<float>((e + 120u) << 23 | m << 20)
-                                        : 0x1p-9f * (float)m;
-  return code & 128u ? -v : v;
+// Codes 2 h and 2 h + 1 of a word, NaN for those of NaN.
+__device__ __forceinline__ void e4m3_values(uint32_t word, int h, float *v) {
+  const auto t = h ? __builtin_amdgcn_cvt_pk_f32_fp8((int)word, true) : __builtin_amdgcn_cvt_pk_f32_fp8((int)word, false);
+  v[0] = t[0];
+  v[1] = t[1];
 }
 
 // The reverse: codes by 16-byte pieces into LDS, rows out of it.
@@ -92,10 +91,13 @@ __global__ __launch_bounds__(kConvThreads) void mx_dequantize_kernel(
     const uint32_t *c = (const uint32_t *)(codes + mx_code_at<FMT>(one, r, lane));
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float u = FMT == SPEAR_MXFP4 ? e2m1_value(c[0] >> (4 * j)) : e4m3_value(c[j >> 2] >> (8 * (j & 3)));
-      v[j] = byte == 255u ? bitcast<float>(0x7FC00000u) : __builtin_amdgcn_ldexpf(u, (int)byte - 127);
+    for (int j = 0; j < 8; j += 2) {
+      if constexpr (FMT == SPEAR_MXFP4) v[j] = e2m1_value(c[0] >> (4 * j)), v[j + 1] = e2m1_value(c[0] >> (4 * j + 4));
+      else e4m3_values(c[j >> 2], j >> 1 & 1, v + j);
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = byte == 255u ? bitcast<float>(0x7FC00000u) : __builtin_amdgcn_ldexpf(v[j], (int)byte - 127);
     store8<DT>(out + (int64_t)row * stride + col, x.cols - col, vec, v);
   }
 }
