@@ -73,8 +73,9 @@ spear_status_t spear_mx_dequantize(const spear_mx_t *x, void *out, int32_t dtype
 /*
  * h = x + residual (fp32; x alone without one), residual_out = h in the type,
  * y = h * r * weight with r = 1 / sqrt(mean(h^2) + eps).  The mean is summed
- * in 64 bits and r rounded once to fp32; the products are fp32, rounded once
- * to the type, or quantized (out_mx).
+ * in 64 bits and r rounded once to fp32 (infinite past its range, 2^128, which
+ * an eps below 2^-256 allows); the products are fp32, rounded once to the type,
+ * or quantized (out_mx).
  *   dtype          SPEAR_F16 or SPEAR_BF16: of x, residual, weight, out.
  *   hidden         1..65536.    rows   0..2^24
  *   strides        between rows, in elements; those of x and residual >= 0.

@@ -182,9 +182,11 @@ template <int XF, int MT>
 hipError_t launch_rows(const MxLinearDesc &d, hipStream_t s) {
   // As many blocks of 16 rows a workgroup (which share what it reads of x, and
   // quantizes) as leave one to a CU, 4 at most, and then as few waves as keep
-  // enough loads in flight.  us, with 1 / 2 / 4 blocks: one token, 4096 rows
-  // of 4096 6.5 / 7.2 / 7.9, 6144 rows 9.4 / 7.8 / 8.6, 11008 rows 13.0 / 13.0 /
-  // 9.5, 28672 rows of 8192 47 / 36 / 28 (4 waves: 26).
+  // enough loads in flight.  us in a graph, e4m3 tokens of a matrix, with 1 / 2 /
+  // 4 blocks and 4 blocks of 4 waves: one token, 4096 rows of 4096 4.6 / 5.2 / 6.6 /
+  // 7.2, 6144 rows 6.7 / 5.6 / 6.9 / 7.7, 11008 rows 9.5 / 8.2 / 8.2 / 8.9, 28672
+  // rows of 8192 35 / 25.0 / 27 / 25.1; 32 tokens 5.7 / 6.4 / 7.8 / 10, 9.0 / 6.7 / 8.2 /
+  // 10, 12.9 / 10.2 / 9.8 / 11 and 48 / 33 / 31 / 28.8.
   constexpr int PER = MT == 1 ? 4 : MT == 2 ? 2 : 1;
   if (d.w.rb <= 256) return launch_from<XF, 1, MT, 16, PER>(d, s);
   if (d.w.rb <= 512) return launch_from<XF, 2, MT, 8, PER>(d, s);
@@ -202,12 +204,21 @@ hipError_t launch_tokens(const MxLinearDesc &d, hipStream_t s) {
 }  // namespace
 
 // Every workgroup quantizes the tokens anew, so a launch that does it once pays
-// from longer rows or more tokens on.  us in a graph, in place / apart, one token
-// and 16: 4096 -> 4096 7.1 / 6.9 and 8.8 / 7.8, 4096 -> 1024 6.3 / 6.5 and 8.1 / 7.2,
-// 11008 -> 4096 13.1 / 11.0 and 16.7 / 11.9, 28672 -> 8192 37 / 30 and 49 / 31; a
-// launch less spares a call of its own 2.
+// from longer rows or more tokens on.  us in a graph, in place / apart, with 1, 4
+// and 8 e4m3 tokens: 2048 -> 1024 4.7 / 5.6, 5.2 / 6.0, 5.5 / 6.0; 2048 -> 11008 7.4 /
+// 8.1, 7.6 / 8.4, 8.0 / 8.6; 4096 -> 4096 7.6 / 7.0, 7.6 / 7.4, 7.9 / 7.5; 4096 ->
+// 28672 17.3 / 18.2, 18.0 / 18.9, 19.0 / 19.2; 8192 -> 4096 10.9 / 9.1, 10.6 / 9.6,
+// 11.2 / 9.5; 8192 -> 28672 29.7 / 28.0, 30.2 / 29.0, 31.9 / 29.1.  (e2m1: 4096 ->
+// 4096 6.0 / 6.4, 6.1 / 6.9, 6.7 / 6.8, -> 28672 16.5 / 15.9, 17.7 / 16.8, 18.9 / 17.0.)
+// As calls of their own a launch less spares 2 up to 4096 columns: 4096 -> 4096
+// 7.9 / 10.6.  So in place where calls gain and a graph loses no more than it gains.
 bool mx_linear_quantizes(int tokens, int cols) { return tokens <= 4 && cols <= 4096 && cols % 128 == 0; }
 
+// Streaming makes 64 tokens at most, and up to there is the faster but for the
+// widest layers.  us in a graph, streamed / tiled, 33, 48 and 64 e4m3 tokens: 4096 ->
+// 4096 8.0 / 11.9, 7.9 / 11.9, 8.4 / 11.9; 4096 -> 11008 11.6 / 12.0, 11.8 / 11.9, 12.1 /
+// 12.0; 11008 -> 4096 16 / 28 each; 8192 -> 28672 35 / 32, 37 / 32, 39 / 35 (where the
+// tiled product is the inexact one; e2m1 27 / 28, 28 / 28, 30 / 29).
 hipError_t launch_mx_linear(const MxLinearDesc &d, hipStream_t s) {
   if (d.x.rows > 64) return launch_mx_gemm(d, s);
   return d.x_format == SPEAR_MXFP4 ? launch_tokens<SPEAR_MXFP4>(d, s) : launch_tokens<SPEAR_MXFP8>(d, s);

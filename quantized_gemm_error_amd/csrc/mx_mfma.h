@@ -28,7 +28,7 @@ __device__ __forceinline__ i32x8_t codes_of_2_and_more(i32x8_t b) {
   return b & ((b >> 6) & 0x01010101) * 255;  // (bytes whose exponent field is 8 or more)
 }
 
-// (Few tokens are bound by the weights' stream, which covers the second
+// (Few tokens are bound by the weights' stream, which covers most of the second
 // product: 28672 rows of 8192, 16 / 32 / 64 tokens 23.9 / 27.3 / 36.8 us with one,
 // 25.2 / 28.7 / 38.5 with two; 4096 x 4096 and one token 4.5 either way.)
 template <int XF>
