@@ -28,7 +28,8 @@ extern "C" {
  *   - and whose weight is at least min_p (the largest weight is 1).
  * The token is the first whose cumulative weight is above u times the weight
  * of all that is kept; its logprob is the logarithm of its own share of it.
- * Weights are summed in 64 bits, in an order that does not depend on timing.
+ * Weights are rounded to 32 places and summed in 64 bits, in an order that does
+ * not depend on timing.
  *
  * A logit of -infinity or NaN is never drawn.  Where a row has logits of
  * +infinity, those alone are drawn, all with weight 1.  A row with nothing to
